@@ -61,6 +61,11 @@ _SIGS = {
     "qsdp_dequantize": (_I, [_P, _P, _P, _I64, _I, _I, _P, _P, _P]),
     "qsdp_error_stats": (_I, [_P, _P, _I64, _P, _P, _P, _P]),
     "qsdp_mean_abs_error": (_I, [_P, _P, _I64, _I, _P, _P, _P]),
+    "kvq_quantize": (_I, [_P, _P, _I, _I64, _I64, _I64, _I64, _I64, _P, _P, _P]),
+    "kvq_dequantize": (_I, [_P, _P, _I64, _P, _P, _I, _P]),
+    "kvq_attention_workspace_bytes": (_SZ, [_I64, _I64, _I, _I, _I]),
+    "kvq_attention": (_I, [_P, _I, _I64, _I, _I64, _I64, _P, _P, _I64, _P, _I64, _I64, _P, _D, _D, _I, _P, _P, _P, _SZ,
+                           _P]),
 }
 
 QSDP_STATS_PARTIALS = 1024
@@ -422,3 +427,135 @@ def qsdp_error_stats(x_bf16, y, ysum, sums, partials, stream=None):
 def qsdp_mean_abs_error(x_bf16, ysum, seeds, out, partials, stream=None):
     _check(load().qsdp_mean_abs_error(_ptr(x_bf16), _ptr(ysum), ysum.numel(), int(seeds), _ptr(out), _ptr(partials),
                                       _stream(stream)), "qsdp_mean_abs_error")
+
+
+# ------------------------------------------------ coded key/value cache
+
+class KvqCache(C.Structure):
+    """kvq_cache_t."""
+    _fields_ = [("k_codes", _P), ("k_scales", _P), ("v_codes", _P), ("v_scales", _P), ("n_pages", _I64),
+                ("page", _I), ("kv_heads", _I), ("head_dim", _I), ("bits", _I)]
+
+
+def _same_device(*tensors):
+    """The one device all the given tensors (None skipped) are on."""
+    devices = {t.device for t in tensors if t is not None}
+    for t in tensors:
+        if t is not None and not t.is_cuda:
+            raise TypeError(f"expected a device (GPU) tensor, got one on {t.device}")
+    if len(devices) != 1:
+        raise ValueError(f"all tensors of a call must be on one device, got {sorted(map(str, devices))}")
+    return devices.pop()
+
+
+def _dense(t, dtype, what):
+    if t.dtype != dtype:
+        raise TypeError(f"{what} must be {dtype}, got {t.dtype}")
+    if not t.is_contiguous():
+        raise ValueError(f"{what} must be contiguous")
+    return t.data_ptr()
+
+
+def _kvq_cache(k_codes, k_scales, v_codes, v_scales, bits):
+    """kvq_cache_t of codes [n_pages, kv_heads, page, head_dim * bits / 8] and scales
+    [n_pages, kv_heads, page]."""
+    import torch
+    if bits not in (4, 8):
+        raise ValueError(f"bits must be 4 or 8, got {bits}")
+    if k_codes.dim() != 4 or k_codes.shape != v_codes.shape:
+        raise ValueError("k_codes and v_codes must both be [n_pages, kv_heads, page, head_dim * bits / 8]")
+    if k_scales.shape != k_codes.shape[:3] or v_scales.shape != k_codes.shape[:3]:
+        raise ValueError("k_scales and v_scales must both be [n_pages, kv_heads, page]")
+    n_pages, heads, page, row = k_codes.shape
+    return KvqCache(_dense(k_codes, torch.uint8, "k_codes"), _dense(k_scales, torch.float32, "k_scales"),
+                    _dense(v_codes, torch.uint8, "v_codes"), _dense(v_scales, torch.float32, "v_scales"),
+                    n_pages, page, heads, row * 8 // bits, bits)
+
+
+def _kvq_rows(t, heads, dim, what):
+    """(token stride, head stride) of [tokens, heads, head_dim] rows whose innermost dimension is dense."""
+    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != dim:
+        raise ValueError(f"{what} must be [tokens, {heads}, {dim}], got {list(t.shape)}")
+    if t.stride(2) != 1:
+        raise ValueError(f"the innermost dimension of {what} must be contiguous")
+    # the stride of a dimension of one entry is never used and may be anything
+    return (t.stride(0) if t.shape[0] > 1 else heads * dim), (t.stride(1) if heads > 1 else dim)
+
+
+def _kvq_slots(slots, tokens):
+    import torch
+    if slots.dim() != 1 or slots.shape[0] != tokens:
+        raise ValueError(f"slots must be [{tokens}], got {list(slots.shape)}")
+    return _dense(slots, torch.int64, "slots")
+
+
+def _kvq_call(name, device, stream, *args):
+    """Run the call with the tensors' device as the current one, on `stream` (default: that
+    device's current stream)."""
+    import torch
+    if stream is not None and not isinstance(stream, int) and stream.device != device:
+        raise ValueError(f"the stream is on {stream.device}, the tensors are on {device}")
+    with torch.cuda.device(device):
+        _check(getattr(load(), name)(*args, _stream(stream)), name)
+
+
+def kvq_quantize(k, v, slots, k_codes, k_scales, v_codes, v_scales, *, bits, stream=None):
+    """k, v: [tokens, kv_heads, head_dim] (any token and head strides); slots: int64 [tokens]."""
+    device = _same_device(k, v, slots, k_codes, k_scales, v_codes, v_scales)
+    cache = _kvq_cache(k_codes, k_scales, v_codes, v_scales, bits)
+    if k.dtype != v.dtype or k.shape != v.shape:
+        raise ValueError("k and v must have one shape and type")
+    kt, kh = _kvq_rows(k, cache.kv_heads, cache.head_dim, "k")
+    vt, vh = _kvq_rows(v, cache.kv_heads, cache.head_dim, "v")
+    _kvq_call("kvq_quantize", device, stream, k.data_ptr(), v.data_ptr(), _dtype_code(k), k.shape[0], kt, kh, vt, vh,
+              _kvq_slots(slots, k.shape[0]), C.byref(cache))
+
+
+def kvq_dequantize(k_codes, k_scales, v_codes, v_scales, slots, k_out, v_out, *, bits, stream=None):
+    """slots: int64 [tokens]; k_out, v_out: contiguous [tokens, kv_heads, head_dim] of one type."""
+    device = _same_device(k_out, v_out, slots, k_codes, k_scales, v_codes, v_scales)
+    cache = _kvq_cache(k_codes, k_scales, v_codes, v_scales, bits)
+    if k_out.dtype != v_out.dtype or k_out.shape != v_out.shape:
+        raise ValueError("k_out and v_out must have one shape and type")
+    _kvq_rows(k_out, cache.kv_heads, cache.head_dim, "k_out")
+    _kvq_call("kvq_dequantize", device, stream, C.byref(cache), _kvq_slots(slots, k_out.shape[0]), k_out.shape[0],
+              _dense(k_out, k_out.dtype, "k_out"), _dense(v_out, v_out.dtype, "v_out"), _dtype_code(k_out))
+
+
+def kvq_attention_workspace_bytes(batch, total_q, q_heads, kv_heads, head_dim) -> int:
+    """Bytes for the current device; 0 for sizes that kvq_attention refuses."""
+    return int(load().kvq_attention_workspace_bytes(int(batch), int(total_q), int(q_heads), int(kv_heads),
+                                                    int(head_dim)))
+
+
+def kvq_attention(q, k_codes, k_scales, v_codes, v_scales, block_table, kv_lens, out, *, bits, workspace, scale=None,
+                  q_offsets=None, softcap=0.0, window=0, lse=None, stream=None):
+    """q: [total_q, q_heads, head_dim] (any token and head strides), bf16 or fp16; block_table: int32
+    [batch, max_pages]; kv_lens: int32 [batch]; out: contiguous, of q's shape and type; q_offsets: int32
+    [batch + 1] (None: total_q / batch rows for every sequence); lse: float32 [total_q, q_heads]; scale:
+    default 1 / sqrt(head_dim)."""
+    import torch
+    device = _same_device(q, k_codes, k_scales, v_codes, v_scales, block_table, kv_lens, out, workspace, q_offsets, lse)
+    cache = _kvq_cache(k_codes, k_scales, v_codes, v_scales, bits)
+    if q.dim() != 3:
+        raise ValueError(f"q must be [total_q, q_heads, head_dim], got {list(q.shape)}")
+    total, q_heads = q.shape[0], q.shape[1]
+    qt, qh = _kvq_rows(q, q_heads, cache.head_dim, "q")
+    if out.dtype != q.dtype or out.shape != q.shape:
+        raise ValueError("out must have q's shape and type")
+    if kv_lens.dim() != 1 or block_table.dim() != 2 or block_table.shape[0] != kv_lens.shape[0]:
+        raise ValueError("kv_lens must be [batch] and block_table [batch, max_pages]")
+    batch, max_pages = block_table.shape
+    if block_table.dtype != torch.int32 or (max_pages > 1 and block_table.stride(1) != 1):
+        raise TypeError("block_table must be int32 with contiguous rows")
+    if q_offsets is not None and list(q_offsets.shape) != [batch + 1]:
+        raise ValueError(f"q_offsets must be [{batch + 1}]")
+    if lse is not None and list(lse.shape) != [total, q_heads]:
+        raise ValueError(f"lse must be [{total}, {q_heads}]")
+    _kvq_call("kvq_attention", device, stream, q.data_ptr(), _dtype_code(q), total, q_heads, qt, qh,
+              None if q_offsets is None else _dense(q_offsets, torch.int32, "q_offsets"),
+              _dense(kv_lens, torch.int32, "kv_lens"), batch, block_table.data_ptr(), max_pages,
+              block_table.stride(0) if batch > 1 else max_pages, C.byref(cache),
+              cache.head_dim ** -0.5 if scale is None else float(scale), float(softcap), int(window),
+              _dense(out, q.dtype, "out"), None if lse is None else _dense(lse, torch.float32, "lse"),
+              _ptr(workspace), workspace.numel() * workspace.element_size())

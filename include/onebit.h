@@ -409,6 +409,98 @@ onebit_status_t qsdp_error_stats(const uint16_t *x_bf16, const float *y, int64_t
 onebit_status_t qsdp_mean_abs_error(const uint16_t *x_bf16, const double *ysum, int64_t n, int seeds,
                                     double *out, double *partials, void *stream);
 
+/* ------------------------------------------------------------------ coded key/value cache
+ * A paged cache of attention keys and values held as signed levels, written, read
+ * back and attended to in its coded form.  A row is the head_dim values of one token
+ * and one cache head.  With L = 2^(bits-1) - 1 and z = 2^(bits-1) (bits 8: 127, 128;
+ * bits 4: 7, 8) and amax = max |x| over the row:
+ *   amax infinite or NaN:  scale = NaN, every code z (the row reads back as NaN)
+ *   amax < 2^-110:         scale = 0,   every code z (the row reads back as 0)
+ *   else  inv = fl32(L / amax),  scale = fl32(amax / L),  code = z + rint(x * inv)
+ * where x * inv is the exact product of the two binary32 numbers and rint takes ties
+ * to even (one rounding; codes lie in z - L .. z + L).  A scale is held at most at the
+ * largest binary32 number with L * scale finite (it matters where amax is within two
+ * units of the last place of binary32's largest number).  The value read back is
+ *   y = fl32((code - z) * scale).
+ *
+ * Layout, all of it contiguous: codes uint8 [n_pages][kv_heads][page][head_dim * bits / 8]
+ * (bits 4: even element in the low nibble), scales fp32 [n_pages][kv_heads][page]; a
+ * pair for keys and a pair for values.  Token t of a sequence is in page
+ * block_table[t / page] of the cache, at offset t % page.  A slot is a token's place
+ * in the whole cache: page number * page + offset.
+ *
+ * bits 4 or 8; head_dim 64, 128 or 256 (ONEBIT_ERR_UNSUPPORTED otherwise); page
+ * a power of two from 16 to 1024; kv_heads from 1 to 32767; n_pages >= 0 and
+ * n_pages * page < 2^47.  Codes and scales are 16-byte aligned.  The struct is a host struct, read
+ * during the call. */
+typedef struct {
+    uint8_t *k_codes;
+    float *k_scales;
+    uint8_t *v_codes;
+    float *v_scales;
+    int64_t n_pages;
+    int page;
+    int kv_heads;
+    int head_dim;
+    int bits;
+} kvq_cache_t;
+
+/* Write `tokens` (below 2^26) rows of keys and values: row i goes to slot slots[i]
+ * (int64 [tokens]).
+ * A slot outside [0, n_pages * page) is skipped: that row is not written (negative
+ * slots are the usual padding).  No slot may occur twice in a call (its row would be
+ * a mixture of the two).  Slots not named keep their codes and scales.
+ * k, v: fp32, bf16 or fp16; value d of head h of row i at k[i * k_token_stride +
+ * h * k_head_stride + d]; strides in elements, 16-byte aligned base, strides that are
+ * multiples of 16 bytes (ONEBIT_ERR_ALIGN otherwise). */
+onebit_status_t kvq_quantize(const void *k, const void *v, onebit_dtype_t dtype, int64_t tokens,
+                             int64_t k_token_stride, int64_t k_head_stride, int64_t v_token_stride,
+                             int64_t v_head_stride, const int64_t *slots, const kvq_cache_t *cache,
+                             void *stream);
+
+/* Read the rows of slots[0 .. tokens) back (tokens below 2^26), rounded once more to bf16 or fp16 when
+ * out_dtype is one of them: k_out, v_out [tokens][kv_heads][head_dim], contiguous,
+ * 16-byte aligned.  A slot outside [0, n_pages * page) leaves its output rows as they
+ * were.  The same slot may occur several times. */
+onebit_status_t kvq_dequantize(const kvq_cache_t *cache, const int64_t *slots, int64_t tokens, void *k_out,
+                               void *v_out, onebit_dtype_t out_dtype, void *stream);
+
+/* Attention of new tokens over the coded cache, which already holds them: from one
+ * token of each sequence to long chunks.  Sequence b has the query rows
+ * q_offsets[b] .. q_offsets[b+1] of q (q_offsets int32 [batch + 1], non-decreasing;
+ * NULL: every sequence has total_q / batch of them) and kv_lens[b] tokens in the cache
+ * (int32 [batch]); its m new tokens are the last m of them, so query t stands at
+ * position p = kv_lens[b] - m + t.  Query head h reads cache head
+ * h / (q_heads / kv_heads).  Over the positions j with p - window < j <= p (window 0:
+ * all j <= p):
+ *   s_j = sm_scale * sum_d q_d k_{j,d};   softcap > 0: s_j = softcap * tanh(s_j / softcap)
+ *   out = sum_j exp(s_j - lse) v_j,       lse = log sum_j exp(s_j)
+ * with k, v the values read back (scaled outside the sums, not rounded).  A query that
+ * attends to nothing (p < 0) gets out = 0 and lse = -inf.  Sums, maxima and lse are
+ * binary32; the weights exp(s_j - max) * v_scale_j enter the second sum as fp16 (11
+ * bits, ties to even) relative to the row's largest.
+ * q: bf16 or fp16 (ONEBIT_ERR_UNSUPPORTED otherwise), addressed as k above.  out:
+ * [total_q][q_heads][head_dim], contiguous, of q's type.  lse: fp32 [total_q][q_heads],
+ * nullable.  Rows of q that belong to no sequence leave out and lse as they were.
+ * block_table: int32, row b at block_table + b * table_stride, max_pages entries of
+ * which are used.  The library never reads outside the given arrays: a length is taken
+ * as 0 if negative and as max_pages * page if larger, a page number outside
+ * [0, n_pages) counts as not attended to, offsets are clamped to 0 .. total_q.  What
+ * the cache holds in positions that are not attended to has no influence, whatever its
+ * bits.  q_heads a multiple of kv_heads; total_q * q_heads and max_pages * page
+ * below 2^31 - 2048; sm_scale finite.
+ * workspace: kvq_attention_workspace_bytes bytes, 16-byte aligned; its contents before
+ * the call do not matter.  Calls that may overlap in time need one each, and so do two
+ * captured graphs that may be replayed at the same time.  (0 is returned for sizes
+ * that kvq_attention refuses.) */
+size_t kvq_attention_workspace_bytes(int64_t batch, int64_t total_q, int q_heads, int kv_heads, int head_dim);
+onebit_status_t kvq_attention(const void *q, onebit_dtype_t dtype, int64_t total_q, int q_heads,
+                              int64_t q_token_stride, int64_t q_head_stride, const int32_t *q_offsets,
+                              const int32_t *kv_lens, int64_t batch, const int32_t *block_table,
+                              int64_t max_pages, int64_t table_stride, const kvq_cache_t *cache,
+                              double sm_scale, double softcap, int window, void *out, float *lse,
+                              void *workspace, size_t workspace_bytes, void *stream);
+
 #ifdef __cplusplus
 }
 #endif
