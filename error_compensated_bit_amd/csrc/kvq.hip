@@ -8,7 +8,6 @@
 // and its maximum a few lane exchanges.  A workgroup takes consecutive tokens of one
 // head: the input rows of a head are far apart anyway (each a whole number of cache
 // lines), while the codes and scales of neighbouring tokens are neighbours in a page.
-#include "device_common.h"
 #include "kvq_common.h"
 
 namespace onebit {
@@ -114,18 +113,6 @@ __global__ __launch_bounds__(kKvqBlock) void k_kvq_quantize(KvqWriteArgs a) {
         *reinterpret_cast<uint32_t *>(a.c.codes[kv] + row * (D / 2) + 4 * sub) = live ? w : 0x88888888u;
     }
     if (sub == 0) a.c.scales[kv][row] = scale;
-}
-
-typedef float f32x2_v __attribute__((ext_vector_type(2)));
-typedef __bf16 bf16x2_v __attribute__((ext_vector_type(2)));
-typedef _Float16 f16x2_v __attribute__((ext_vector_type(2)));
-
-// two fp32 values rounded to nearest even, first in the low half
-template <int GT>
-__device__ __forceinline__ uint32_t round_pair(float a, float b) {
-    const f32x2_v v = {a, b};
-    if (GT == kGradBF16) return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bf16x2_v));
-    return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, f16x2_v));
 }
 
 template <int GT, int D, int BITS>

@@ -3,33 +3,11 @@
 // with kc, vc the codes and ks, vs the scales of the attended rows.
 #include <math.h>
 
-#include "device_common.h"
-#include "kvq_common.h"
+#include <algorithm>
+
+#include "kvq_step.h"
 
 namespace onebit {
-
-struct KvqAttnArgs {
-    KvqCache c;
-    const uint16_t *q;
-    uint16_t *out;
-    float *lse;
-    int64_t q_token_stride, q_head_stride;
-    const int32_t *q_offsets;
-    const int32_t *kv_lens;
-    const int32_t *table;
-    int64_t table_stride;
-    int32_t batch, total_q, q_heads, group;
-    int32_t max_tokens;  // max_pages * page
-    int32_t q_uniform;   // query rows of every sequence where q_offsets is null
-    int32_t window;
-    float scale;    // sm_scale
-    float softcap;  // 0: none
-};
-
-__device__ __forceinline__ int32_t seq_begin(const KvqAttnArgs &a, int b) {
-    if (!a.q_offsets) return b * a.q_uniform;
-    return min(max(a.q_offsets[b], 0), a.total_q);
-}
 
 template <int GT, int D, int BITS>
 __global__ __launch_bounds__(256) void k_kvq_attention(KvqAttnArgs a) {
@@ -42,13 +20,12 @@ __global__ __launch_bounds__(256) void k_kvq_attention(KvqAttnArgs a) {
     int lo = 0, hi = a.batch;
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
-        if (seq_begin(a, mid) <= row) lo = mid; else hi = mid;
+        if (kvq_seq(a, mid).q0 <= row) lo = mid; else hi = mid;
     }
-    const int b = lo, q0 = seq_begin(a, b), q1 = seq_begin(a, b + 1);
-    if (row < q0 || row >= q1) return;
-    const int kv = min(max(a.kv_lens[b], 0), a.max_tokens);
-    const int64_t p = (int64_t)kv - (q1 - q0) + (row - q0);
-    const int end = (int)(p + 1), begin = a.window > 0 ? (int)max((int64_t)0, p - a.window + 1) : 0;
+    const int b = lo;
+    const KvqSeq seq = kvq_seq(a, b);
+    if (row < seq.q0 || row >= seq.q0 + seq.len || (int64_t)seq.len * a.group <= a.max_rows) return;
+    const int end = kvq_hi(seq, row - seq.q0), begin = kvq_lo(a, seq, row - seq.q0);
     float q[V], o[V], m = -INFINITY, l = 0.0f;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
@@ -74,9 +51,10 @@ __global__ __launch_bounds__(256) void k_kvq_attention(KvqAttnArgs a) {
         }
 #pragma unroll
         for (int x = 32; x >= 1; x >>= 1) s += __shfl_xor(s, x, 64);
-        s *= a.c.scales[0][r] * a.scale;
-        if (a.softcap > 0.0f) s = a.softcap * tanhf(s / a.softcap);
-        const float mn = fmaxf(m, s), f = expf(m - mn), e = expf(s - mn);
+        s *= a.c.scales[0][r] * a.scale2;
+        if (a.q_sign) s = -s;
+        if (a.cap2 > 0.0f) s = capped(s * a.cap_scale, a.cap2);
+        const float mn = fmaxf(m, s), f = exp2f(m - mn), e = exp2f(s - mn);
         const float w = e * a.c.scales[1][r];
         l = l * f + e;
 #pragma unroll
@@ -94,34 +72,68 @@ __global__ __launch_bounds__(256) void k_kvq_attention(KvqAttnArgs a) {
     float mm = s_m[0];
     for (int w = 1; w < 4; ++w) mm = fmaxf(mm, s_m[w]);
     float ll = 0.0f;
-    for (int w = 0; w < 4; ++w) ll += s_l[w] > 0.0f || s_l[w] != s_l[w] ? s_l[w] * expf(s_m[w] - mm) : 0.0f;
+    for (int w = 0; w < 4; ++w) ll += s_l[w] > 0.0f || s_l[w] != s_l[w] ? s_l[w] * exp2f(s_m[w] - mm) : 0.0f;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
         float t = 0.0f;
         for (int w = 0; w < 4; ++w)
-            if (s_l[w] != 0.0f) t += s_o[w][lane * V + v] * expf(s_m[w] - mm);
+            if (s_l[w] != 0.0f) t += s_o[w][lane * V + v] * exp2f(s_m[w] - mm);
         t = ll != 0.0f ? t / ll : 0.0f;
         const _Float16 th = (_Float16)t;
         a.out[((int64_t)row * a.q_heads + h) * D + lane * V + v] =
             GT == kGradBF16 ? (uint16_t)float_to_bf16_bits(t) : __builtin_bit_cast(uint16_t, th);
     }
-    if (a.lse && lane == 0) a.lse[(int64_t)row * a.q_heads + h] = ll != 0.0f ? mm + logf(ll) : -INFINITY;
+    if (a.lse && lane == 0) a.lse[(int64_t)row * a.q_heads + h] = ll != 0.0f ? (mm + log2f(ll)) * 0.693147180559945f : -INFINITY;
+}
+
+// Workgroups of a launch of the step kernel: two for each compute unit.
+static int step_groups() {
+    int dev = 0, cus = 256;
+    if (hipGetDevice(&dev) == hipSuccess) {
+        int v = 0;
+        if (hipDeviceGetAttribute(&v, hipDeviceAttributeMultiprocessorCount, dev) == hipSuccess && v > 0) cus = v;
+    }
+    return std::min(2 * cus, kStepMaxGroups);
 }
 
 static size_t attention_workspace(int64_t batch, int64_t total_q, int q_heads, int kv_heads, int head_dim) {
     if (batch < 0 || total_q < 0 || q_heads < 1 || kv_heads < 1 || q_heads % kv_heads || kv_heads > 32767) return 0;
     if (head_dim != 64 && head_dim != 128 && head_dim != 256) return 0;
     if (batch >= (1 << 26) || total_q > (0x7fffffff - 2048) / q_heads) return 0;
-    return 256;
+    const size_t rows = head_dim == 256 ? 16 : 32;
+    return kStepHeader + (size_t)step_groups() * 2 * rows * (head_dim + 2) * sizeof(float);
+}
+
+template <int GT, int D, int BITS>
+static void launch(KvqAttnArgs a, hipStream_t s) {
+    constexpr int kWide = D == 256 ? 1 : 2;
+    a.max_rows = 32;
+    if (a.q_offsets || (int64_t)a.q_uniform * a.group > a.max_rows)
+        hipLaunchKernelGGL((k_kvq_attention<GT, D, BITS>), dim3(a.total_q, a.q_heads), dim3(256), 0, s, a);
+    if (!a.q_offsets && (int64_t)a.q_uniform * a.group > a.max_rows) return;
+    const bool wide = kWide == 2 && (a.group > 16 || (!a.q_offsets && a.q_uniform * a.group > 16));
+    const unsigned groups = (unsigned)step_groups();
+    const int batch = a.batch;
+    for (int b = 0; b < batch; b += kStepSeqs) {
+        KvqAttnArgs x = a;
+        x.batch = std::min(batch - b, kStepSeqs);
+        if (a.q_offsets) x.q_offsets = a.q_offsets + b;
+        x.kv_lens = a.kv_lens + b;
+        x.table = a.table + b * a.table_stride;
+        x.q_first = b * a.q_uniform;
+        if (wide)
+            hipLaunchKernelGGL((k_kvq_step<GT, D, BITS, kWide>), dim3(groups), dim3(kStepBlock), 0, s, x);
+        else
+            hipLaunchKernelGGL((k_kvq_step<GT, D, BITS, 1>), dim3(groups), dim3(kStepBlock), 0, s, x);
+    }
 }
 
 template <int GT, int D>
 static void launch_bits(int bits, const KvqAttnArgs &a, hipStream_t s) {
-    const dim3 grid(a.total_q, a.q_heads);
     if (bits == 4)
-        hipLaunchKernelGGL((k_kvq_attention<GT, D, 4>), grid, dim3(256), 0, s, a);
+        launch<GT, D, 4>(a, s);
     else
-        hipLaunchKernelGGL((k_kvq_attention<GT, D, 8>), grid, dim3(256), 0, s, a);
+        launch<GT, D, 8>(a, s);
 }
 template <int GT>
 static void launch_dim(int dim, int bits, const KvqAttnArgs &a, hipStream_t s) {
@@ -179,11 +191,15 @@ extern "C" onebit_status_t kvq_attention(const void *q, onebit_dtype_t dtype, in
     a.total_q = (int32_t)total_q;
     a.q_heads = q_heads;
     a.group = q_heads / cache->kv_heads;
-    a.max_tokens = (int32_t)(max_pages * cache->page);
+    // without pages there is nothing to read, whatever the table says
+    a.max_tokens = a.c.n_pages ? (int32_t)(max_pages * cache->page) : 0;
     a.q_uniform = q_offsets ? 0 : (int32_t)(total_q / batch);
     a.window = window;
-    a.scale = (float)sm_scale;
-    a.softcap = (float)softcap;
+    a.scale2 = (float)(__builtin_fabs(sm_scale) * 1.4426950408889634);
+    a.q_sign = sm_scale < 0.0 ? 0x80000000u : 0u;
+    a.cap2 = (float)(softcap * 1.4426950408889634);
+    a.cap_scale = softcap > 0.0 ? (float)(2.0 / softcap) : 0.0f;
+    a.workspace = workspace;
     hipStream_t s = static_cast<hipStream_t>(stream);
     if (dtype == ONEBIT_BF16)
         launch_dim<kGradBF16>(cache->head_dim, cache->bits, a, s);

@@ -5,6 +5,7 @@
 
 #include <hip/hip_runtime.h>
 
+#include "device_common.h"
 #include "internal.h"
 #include "onebit.h"
 
@@ -29,6 +30,18 @@ struct KvqLevels {
     // the largest fp32 number with L times it finite: amax / L rounded up can pass it
     static constexpr float kMaxScale = BITS == 8 ? 0x1.020406p+121f : 0x1.249248p+125f;
 };
+
+typedef float f32x2_v __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x2_v __attribute__((ext_vector_type(2)));
+typedef _Float16 f16x2_v __attribute__((ext_vector_type(2)));
+
+// two fp32 values rounded to nearest even, first in the low half
+template <int GT>
+__device__ __forceinline__ uint32_t round_pair(float a, float b) {
+    const f32x2_v v = {a, b};
+    if (GT == kGradBF16) return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bf16x2_v));
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, f16x2_v));
+}
 
 // Checks of a caller's cache; fills *out.  Pointers are needed only where there are pages.
 inline onebit_status_t kvq_check_cache(const kvq_cache_t *c, KvqCache *out) {

@@ -489,10 +489,11 @@ onebit_status_t kvq_dequantize(const kvq_cache_t *cache, const int64_t *slots, i
  * the cache holds in positions that are not attended to has no influence, whatever its
  * bits.  q_heads a multiple of kv_heads; total_q * q_heads and max_pages * page
  * below 2^31 - 2048; sm_scale finite.
- * workspace: kvq_attention_workspace_bytes bytes, 16-byte aligned; its contents before
- * the call do not matter.  Calls that may overlap in time need one each, and so do two
- * captured graphs that may be replayed at the same time.  (0 is returned for sizes
- * that kvq_attention refuses.) */
+ * workspace: kvq_attention_workspace_bytes bytes (on the device that is current), 16-byte
+ * aligned, zeroed once before its first use (onebit_workspace_init); every completed
+ * call leaves it ready for the next one, of any sizes it is large enough for.  Calls
+ * that may overlap in time need one each, and so do two captured graphs that may be
+ * replayed at the same time.  (0 is returned for sizes that kvq_attention refuses.) */
 size_t kvq_attention_workspace_bytes(int64_t batch, int64_t total_q, int q_heads, int kv_heads, int head_dim);
 onebit_status_t kvq_attention(const void *q, onebit_dtype_t dtype, int64_t total_q, int q_heads,
                               int64_t q_token_stride, int64_t q_head_stride, const int32_t *q_offsets,

@@ -52,11 +52,14 @@ def attention(q, pools, table, kv_lens, *, bits, scale, q_offsets=None, softcap=
     The tolerance counts, per row and output element, with A = sum_j softmax_j |v_j|:
       - the weights' rounding to fp16, 2^-11 of each term: 2^-11 A (their sum and the rounded
         terms' own weights cancel no better than that);
-      - the scores: D products and their sum in fp32 and a few scalings, (D + 8) 2^-24 of
-        sum_d |q_d k_d| each; exp2's argument is rounded at the size of the score itself and exp2 is
-        good to an ulp: 2^-22 (|s| + 1); a capped score is off by 2^-21 cap.  An error e of every
-        score moves each weight and their sum by e: 2 e A;
-      - the sums over n terms in fp32: (n + 64) 2^-24, twice.
+      - the scores: D products and their sum in fp32 and a few scalings.  The sum is of codes, as
+        exact as if each were 1024 (8 bits) or 64 (4 bits) in place of c - z, that is R = 1024 or 64
+        scales in place of k_d: (D + 8) 2^-24 R scale_j sum_d |q_d| each.  exp2's argument is
+        rounded at the size of the score itself and exp2 is good to an ulp: 2^-22 (|s| + 1); a
+        capped score is off by 2^-21 cap.  An error e of every score moves each weight and their sum
+        by e: 2 e A;
+      - the sums over n terms in fp32, of codes too: (n + 64) 2^-24 (A + R sum_j softmax_j scale_j),
+        twice.
     Weights far below the row's largest lose bits to fp16's range: 2^-31 of the largest
     scale's row for each of the n terms.  lse is off by what the scores are, the sum's n roundings
     and its own (2^-22 of its size).
@@ -66,7 +69,7 @@ def attention(q, pools, table, kv_lens, *, bits, scale, q_offsets=None, softcap=
     total, hq, dim = q.shape
     group = hq // heads
     batch, max_pages = table.shape
-    top, z = LEVELS[bits]
+    top, reach = LEVELS[bits][0], {8: 1024.0, 4: 64.0}[bits]
     out = torch.zeros(total, hq, dim, dtype=torch.float64)
     tol = torch.zeros(total, hq, dim, dtype=torch.float64)
     lse = torch.full((total, hq), -math.inf, dtype=torch.float64)
@@ -97,7 +100,7 @@ def attention(q, pools, table, kv_lens, *, bits, scale, q_offsets=None, softcap=
             for h in range(g * group, (g + 1) * group):
                 x = q[lo:hi, h].double()
                 s = scale * (x @ k.T)
-                size = abs(scale) * (x.abs() @ k.abs().T)
+                size = abs(scale) * reach * x.abs().sum(1, keepdim=True) * ks.double().abs()
                 off = (dim + 8) * 2.0 ** -24 * size + 2.0 ** -22 * (s.abs() + 1)
                 if softcap:
                     s = softcap * torch.tanh(s / softcap)
@@ -115,6 +118,7 @@ def attention(q, pools, table, kv_lens, *, bits, scale, q_offsets=None, softcap=
                 count = keep.sum(1, keepdim=True).double()
                 a = p @ v.abs()
                 lse_tol[lo:hi, h] = (worst + (count + 64) * 2.0 ** -24).squeeze(1) + 2.0 ** -22 * (lse[lo:hi, h].abs() + 1)
-                tol[lo:hi, h] = a * (2.0 ** -11 + 2 * worst + 2 * (count + 64) * 2.0 ** -24) + \
+                wide = a + reach * (p @ vs.double().abs()).unsqueeze(1)
+                tol[lo:hi, h] = a * (2.0 ** -11 + 2 * worst) + 2 * (count + 64) * 2.0 ** -24 * wide + \
                     count * 2.0 ** -31 * float(torch.nan_to_num(vs).max()) * top
     return out, lse, tol, lse_tol, owned

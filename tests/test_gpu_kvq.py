@@ -164,8 +164,7 @@ def attend(q, pools, table, kv_lens, bits, *, scale=None, q_offsets=None, softca
     out = torch.full((total, hq, dim), fill, dtype=q.dtype, device=DEV)
     l = torch.full((total, hq), fill, device=DEV) if lse else None
     size = ob.kvq_attention_workspace_bytes(len(kv_lens), total, hq, pools[0].shape[1], dim)
-    # whatever the workspace holds
-    ws = torch.full((size,), 0xff, dtype=torch.uint8, device=DEV)
+    ws = torch.zeros(size, dtype=torch.uint8, device=DEV)
     pd = dev(pools)
     ob.kvq_attention(q.to(DEV) if qd is None else qd, *pd, table.to(DEV), kv_lens.to(DEV), out, bits=bits, scale=scale,
                      q_offsets=None if q_offsets is None else q_offsets.to(DEV), softcap=softcap, window=window, lse=l,
@@ -546,7 +545,7 @@ def test_a_prompt_in_chunks_then_generation(bits, dtype):
         q, k, v = d[:, :hq], d[:, hq:hq + heads], d[:, hq + heads:]
         ob.kvq_quantize(k, v, slots.to(DEV), *pools, bits=bits)
         out = torch.empty(total, hq, dim, dtype=dtype, device=DEV)
-        ws = torch.empty(ob.kvq_attention_workspace_bytes(batch, total, hq, heads, dim), dtype=torch.uint8, device=DEV)
+        ws = torch.zeros(ob.kvq_attention_workspace_bytes(batch, total, hq, heads, dim), dtype=torch.uint8, device=DEV)
         ob.kvq_attention(q, *pools, table.to(DEV), lens.to(DEV), out, bits=bits, q_offsets=offs.to(DEV), workspace=ws)
         ko, vo = (torch.empty(total, heads, dim, device=DEV) for _ in range(2))
         ob.kvq_dequantize(*pools, slots.to(DEV), ko, vo, bits=bits)
@@ -616,7 +615,7 @@ def test_two_calls_at_once_on_two_streams():
     size = ob.kvq_attention_workspace_bytes(5, q.shape[0], 8, 2, 128)
     streams = [torch.cuda.Stream() for _ in range(2)]
     outs = [[torch.empty_like(qd) for _ in range(8)] for _ in streams]
-    wss = [torch.empty(size, dtype=torch.uint8, device=DEV) for _ in streams]
+    wss = [torch.zeros(size, dtype=torch.uint8, device=DEV) for _ in streams]
     torch.cuda.synchronize()
     for i in range(8):
         for s, o, ws in zip(streams, outs, wss):
