@@ -125,12 +125,33 @@ __device__ __forceinline__ uint32_t code_pair(uint32_t wa, uint32_t wb, int u) {
     return ((u & 1) ? x : x << 4) & 0x00f000f0u;
 }
 
+// Weights are rounded to fp16 (11 bits) for the matrix cores.  For bf16 outputs that is
+// an eighth of the output's own rounding; an fp16 output would come out 1.6 times as
+// far off (measured), so there what the rounding drops goes through the matrix cores
+// as a second fp16 operand.
+template <int GT>
+constexpr bool kTwoPart = GT == kGradF16;
+
+__device__ __forceinline__ float add_pair(uint32_t pair, float sum) {
+    return __builtin_amdgcn_fdot2(__builtin_bit_cast(f16x2_v, pair), (f16x2_v){(_Float16)1, (_Float16)1}, sum, false);
+}
+__device__ __forceinline__ uint32_t rest_pair(float a, float b, uint32_t pair) {
+    const f16x2_v h = __builtin_bit_cast(f16x2_v, pair);
+    return round_pair<kGradF16>(a - (float)h[0], b - (float)h[1]);  // both differences exact
+}
+
 // Exponent k that brings a row of queries whose largest magnitude is amax to
 // [2^14, 2^15) as fp16: exact for bf16 and fp16 values down to 2^-29 of the largest,
 // and smaller ones are off by less than 2^-39 of it.
 __device__ __forceinline__ int query_exponent(float amax) {
     const int e = (int)((__float_as_uint(amax) >> 23) & 255u) - 127;  // zero and subnormal: -127
     return min(14 - e, 120);
+}
+
+// a / b for a >= 0, b > 0: the 64-bit division only where it is needed
+__device__ __forceinline__ int64_t udiv(int64_t a, int64_t b) {
+    if (((a | b) >> 32) == 0) return (uint32_t)a / (uint32_t)b;
+    return a / b;
 }
 
 // the value every lane of the wave holds, as a scalar

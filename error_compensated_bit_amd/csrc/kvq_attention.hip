@@ -86,14 +86,14 @@ __global__ __launch_bounds__(256) void k_kvq_attention(KvqAttnArgs a) {
     if (a.lse && lane == 0) a.lse[(int64_t)row * a.q_heads + h] = ll != 0.0f ? (mm + log2f(ll)) * 0.693147180559945f : -INFINITY;
 }
 
-// Workgroups of a launch of the step kernel: two for each compute unit.
+// Workgroups of a launch of the step kernel: three for each compute unit.
 static int step_groups() {
     int dev = 0, cus = 256;
     if (hipGetDevice(&dev) == hipSuccess) {
         int v = 0;
         if (hipDeviceGetAttribute(&v, hipDeviceAttributeMultiprocessorCount, dev) == hipSuccess && v > 0) cus = v;
     }
-    return std::min(2 * cus, kStepMaxGroups);
+    return std::min(3 * cus, kStepMaxGroups);
 }
 
 static size_t attention_workspace(int64_t batch, int64_t total_q, int q_heads, int kv_heads, int head_dim) {
