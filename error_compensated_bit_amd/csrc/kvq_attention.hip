@@ -5,126 +5,76 @@
 
 #include <algorithm>
 
+#include "kvq_chunk.h"
 #include "kvq_step.h"
 
 namespace onebit {
 
-template <int GT, int D, int BITS>
-__global__ __launch_bounds__(256) void k_kvq_attention(KvqAttnArgs a) {
-    constexpr int V = D / 64;
-    __shared__ float s_o[4][D];
-    __shared__ float s_m[4], s_l[4];
-    const int row = blockIdx.x, h = blockIdx.y, g = h / a.group;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    // the last sequence that begins at or before the row
-    int lo = 0, hi = a.batch;
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (kvq_seq(a, mid).q0 <= row) lo = mid; else hi = mid;
-    }
-    const int b = lo;
-    const KvqSeq seq = kvq_seq(a, b);
-    if (row < seq.q0 || row >= seq.q0 + seq.len || (int64_t)seq.len * a.group <= a.max_rows) return;
-    const int end = kvq_hi(seq, row - seq.q0), begin = kvq_lo(a, seq, row - seq.q0);
-    float q[V], o[V], m = -INFINITY, l = 0.0f;
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-        q[v] = half_bits_to_float<GT>(a.q[row * a.q_token_stride + h * a.q_head_stride + lane * V + v]);
-        o[v] = 0.0f;
-    }
-    for (int j = begin + wave; j < end; j += 4) {
-        const int64_t page = a.table[b * a.table_stride + (j >> a.c.shift)];
-        if (page < 0 || page >= a.c.n_pages) continue;
-        const int64_t r = (page * a.c.heads + g) * a.c.page + (j & (a.c.page - 1));
-        float kc[V], vc[V], s = 0.0f;
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            const int d = lane * V + v;
-            if (BITS == 8) {
-                kc[v] = (float)a.c.codes[0][r * D + d];
-                vc[v] = (float)a.c.codes[1][r * D + d];
-            } else {
-                kc[v] = (float)((a.c.codes[0][r * (D / 2) + (d >> 1)] >> (4 * (d & 1))) & 15);
-                vc[v] = (float)((a.c.codes[1][r * (D / 2) + (d >> 1)] >> (4 * (d & 1))) & 15);
-            }
-            s = fmaf(q[v], kc[v] - (float)KvqLevels<BITS>::kZero, s);
-        }
-#pragma unroll
-        for (int x = 32; x >= 1; x >>= 1) s += __shfl_xor(s, x, 64);
-        s *= a.c.scales[0][r] * a.scale2;
-        if (a.q_sign) s = -s;
-        if (a.cap2 > 0.0f) s = capped(s * a.cap_scale, a.cap2);
-        const float mn = fmaxf(m, s), f = exp2f(m - mn), e = exp2f(s - mn);
-        const float w = e * a.c.scales[1][r];
-        l = l * f + e;
-#pragma unroll
-        for (int v = 0; v < V; ++v) o[v] = fmaf(w, vc[v] - (float)KvqLevels<BITS>::kZero, o[v] * f);
-        m = mn;
-    }
-    if (lane == 0) {
-        s_m[wave] = m;
-        s_l[wave] = l;
-    }
-#pragma unroll
-    for (int v = 0; v < V; ++v) s_o[wave][lane * V + v] = o[v];
-    __syncthreads();
-    if (wave) return;
-    float mm = s_m[0];
-    for (int w = 1; w < 4; ++w) mm = fmaxf(mm, s_m[w]);
-    float ll = 0.0f;
-    for (int w = 0; w < 4; ++w) ll += s_l[w] > 0.0f || s_l[w] != s_l[w] ? s_l[w] * exp2f(s_m[w] - mm) : 0.0f;
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-        float t = 0.0f;
-        for (int w = 0; w < 4; ++w)
-            if (s_l[w] != 0.0f) t += s_o[w][lane * V + v] * exp2f(s_m[w] - mm);
-        t = ll != 0.0f ? t / ll : 0.0f;
-        const _Float16 th = (_Float16)t;
-        a.out[((int64_t)row * a.q_heads + h) * D + lane * V + v] =
-            GT == kGradBF16 ? (uint16_t)float_to_bf16_bits(t) : __builtin_bit_cast(uint16_t, th);
-    }
-    if (a.lse && lane == 0) a.lse[(int64_t)row * a.q_heads + h] = ll != 0.0f ? (mm + log2f(ll)) * 0.693147180559945f : -INFINITY;
-}
-
-// Workgroups of a launch of the step kernel: three for each compute unit.
-static int step_groups() {
+static int compute_units() {
     int dev = 0, cus = 256;
     if (hipGetDevice(&dev) == hipSuccess) {
         int v = 0;
         if (hipDeviceGetAttribute(&v, hipDeviceAttributeMultiprocessorCount, dev) == hipSuccess && v > 0) cus = v;
     }
-    return std::min(3 * cus, kStepMaxGroups);
+    return cus;
+}
+
+// Workgroups of a launch: as many as are resident at once.
+static int step_groups() { return std::min(3 * compute_units(), kStepMaxGroups); }
+static int chunk_groups() { return std::min(compute_units(), kChunkMaxGroups); }
+
+constexpr int kChunkWaves = 8;
+// The step kernel's counters, then the partial results of either kernel (one runs after
+// the other).
+static size_t step_bytes(int dim) {
+    return (size_t)step_groups() * 2 * (dim == 256 ? 16 : 32) * (dim + 2) * sizeof(float);
+}
+static size_t chunk_bytes(int dim) {
+    return kChunkMaxGroups * sizeof(ChunkSplit) +
+           (size_t)chunk_groups() * 2 * kChunkWaves * 32 * (dim + 2) * sizeof(float);
 }
 
 static size_t attention_workspace(int64_t batch, int64_t total_q, int q_heads, int kv_heads, int head_dim) {
     if (batch < 0 || total_q < 0 || q_heads < 1 || kv_heads < 1 || q_heads % kv_heads || kv_heads > 32767) return 0;
     if (head_dim != 64 && head_dim != 128 && head_dim != 256) return 0;
     if (batch >= (1 << 26) || total_q > (0x7fffffff - 2048) / q_heads) return 0;
-    const size_t rows = head_dim == 256 ? 16 : 32;
-    return kStepHeader + (size_t)step_groups() * 2 * rows * (head_dim + 2) * sizeof(float);
+    return kStepHeader + std::max(step_bytes(head_dim), chunk_bytes(head_dim));
+}
+
+// The sequences [b, b + count) of a call, as a launch's own.
+static KvqAttnArgs slice(const KvqAttnArgs &a, int b, int count) {
+    KvqAttnArgs x = a;
+    x.batch = std::min(a.batch - b, count);
+    if (a.q_offsets) x.q_offsets = a.q_offsets + b;
+    x.kv_lens = a.kv_lens + b;
+    x.table = a.table + b * a.table_stride;
+    x.q_first = b * a.q_uniform;
+    return x;
 }
 
 template <int GT, int D, int BITS>
 static void launch(KvqAttnArgs a, hipStream_t s) {
     constexpr int kWide = D == 256 ? 1 : 2;
     a.max_rows = 32;
-    if (a.q_offsets || (int64_t)a.q_uniform * a.group > a.max_rows)
-        hipLaunchKernelGGL((k_kvq_attention<GT, D, BITS>), dim3(a.total_q, a.q_heads), dim3(256), 0, s, a);
-    if (!a.q_offsets && (int64_t)a.q_uniform * a.group > a.max_rows) return;
-    const bool wide = kWide == 2 && (a.group > 16 || (!a.q_offsets && a.q_uniform * a.group > 16));
-    const unsigned groups = (unsigned)step_groups();
-    const int batch = a.batch;
-    for (int b = 0; b < batch; b += kStepSeqs) {
-        KvqAttnArgs x = a;
-        x.batch = std::min(batch - b, kStepSeqs);
-        if (a.q_offsets) x.q_offsets = a.q_offsets + b;
-        x.kv_lens = a.kv_lens + b;
-        x.table = a.table + b * a.table_stride;
-        x.q_first = b * a.q_uniform;
-        if (wide)
-            hipLaunchKernelGGL((k_kvq_step<GT, D, BITS, kWide>), dim3(groups), dim3(kStepBlock), 0, s, x);
-        else
-            hipLaunchKernelGGL((k_kvq_step<GT, D, BITS, 1>), dim3(groups), dim3(kStepBlock), 0, s, x);
+    const int64_t rows = (int64_t)a.q_uniform * a.group;  // of every sequence, where that is known
+    if (a.q_offsets || rows <= a.max_rows) {
+        const bool wide = kWide == 2 && (a.group > 16 || (!a.q_offsets && rows > 16));
+        for (int b = 0; b < a.batch; b += kStepSeqs) {
+            const KvqAttnArgs x = slice(a, b, kStepSeqs);
+            if (wide)
+                hipLaunchKernelGGL((k_kvq_step<GT, D, BITS, kWide>), dim3(step_groups()), dim3(kStepBlock), 0, s, x);
+            else
+                hipLaunchKernelGGL((k_kvq_step<GT, D, BITS, 1>), dim3(step_groups()), dim3(kStepBlock), 0, s, x);
+        }
+    }
+    // without offsets that say otherwise, no sequence has more than all the rows
+    if (a.q_offsets ? (int64_t)a.total_q * a.group > a.max_rows : rows > a.max_rows) {
+        for (int b = 0; b < a.batch; b += kChunkSeqs) {
+            KvqAttnArgs x = slice(a, b, kChunkSeqs);
+            x.workspace = static_cast<char *>(a.workspace) + kStepHeader;
+            hipLaunchKernelGGL((k_kvq_chunk<GT, D, BITS, kChunkWaves>), dim3(chunk_groups()), dim3(64 * kChunkWaves), 0, s, x);
+            hipLaunchKernelGGL((k_kvq_chunk_join<GT, D, kChunkWaves>), dim3(chunk_groups(), kChunkWaves), dim3(256), 0, s, x);
+        }
     }
 }
 

@@ -1,0 +1,636 @@
+// kvq_chunk.h -- attention of chunks of new tokens over the coded cache: bound by the
+// matrix products and the softmax between them.
+//
+// A workgroup takes 32 query rows (tokens x heads of one cache head) for each of its
+// waves and walks the cache in tiles.  A tile's codes are loaded two tiles ahead,
+// expanded to fp16 once for all rows while the tile before is worked on, and kept in
+// LDS twice over (one barrier a tile): keys by token, values by dimension, so that
+// both are read back as whole operands of v_mfma_f32_32x32x16_f16.  S^T = K Q^T and
+// O^T = V^T P^T: as in the step kernel, a query row stays in its lane from the scores
+// to the output.
+//
+// For bf16 the rows are expanded to (c - z) scale 2^k, rounded to fp16: one step in
+// 2^11 of a value, where a code of 8 bits is one in 2^8 of the row's largest.  Then the
+// scores need one fused operation and one exponential each.  For fp16 the operands are
+// the codes (c - z) themselves, exact, and the scales are applied to scores and weights
+// in fp32, because an fp16 output would show those roundings.
+//
+// The work is one line of tiles, shared out and joined as in the step kernel, except
+// that a second small kernel joins the partial results (a workgroup's is too large to
+// be read back by one).
+#pragma once
+
+#include "kvq_attention.h"
+
+namespace onebit {
+
+constexpr int kChunkSeqs = 512;        // sequences of one launch
+constexpr int kChunkMaxGroups = 1024;  // workgroups of one launch
+
+// What workgroup w leaves for the join of the item that it begins and does not end.
+struct ChunkSplit {
+    int32_t last;   // the item's last workgroup; -1: there is no such item
+    int32_t slot;   // of its first part
+    int32_t seq, tile, head;
+    int32_t pad[3];
+};
+
+template <int GT, int D, int NW>
+struct ChunkPartial {
+    float o[NW][D / 2][64];  // [wave][register][lane]
+    float ml[NW][32][2];     // rows' maxima and sums
+};
+
+template <int GT, int D, int BITS, int NW>
+struct ChunkShape {
+    static constexpr bool kExact = GT == kGradF16;
+    static constexpr int kThreads = 64 * NW, kRows = 32 * NW;
+    static constexpr int kTile = D == 256 ? 32 : D == 128 ? 64 : 128;  // tokens
+    static constexpr int kSub = kTile < 64 ? kTile : 64;               // tokens of one softmax step
+    static constexpr int kItems = kTile * D / 16 / kThreads;           // rows' pieces a thread expands
+    static constexpr int kKeyRow = D + 8;                              // fp16 elements; 16 bytes of padding
+    static constexpr int kValRow = kTile + 8;                          // spread the rows over the banks
+    static constexpr int kCodeWords = BITS / 2;                        // words of 16 codes
+    static_assert(kItems >= 1 && kItems * kThreads == kTile * D / 16, "every thread expands whole pieces");
+};
+
+__device__ __forceinline__ f16x2_v splat16(float v) {
+    const _Float16 h = (_Float16)v;
+    return (f16x2_v){h, h};
+}
+__device__ __forceinline__ uint32_t fma16(uint32_t codes, f16x2_v scale, f16x2_v offset) {
+    return __builtin_bit_cast(uint32_t, __builtin_elementwise_fma(__builtin_bit_cast(f16x2_v, codes), scale, offset));
+}
+
+// 16 consecutive codes to fp16, in the order of query_operand
+template <int BITS>
+__device__ __forceinline__ void expand16(const uint32_t (&w)[BITS / 2], f16x2_v scale, f16x2_v offset, uint4 (&out)[2]) {
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        const u32x4_v c = __builtin_bit_cast(
+            u32x4_v, codes_over_dims<BITS>(w[BITS == 8 ? 2 * k : k], w[BITS == 8 ? 2 * k + 1 : k]));
+        out[k] = make_uint4(fma16(c.x, scale, offset), fma16(c.y, scale, offset), fma16(c.z, scale, offset),
+                            fma16(c.w, scale, offset));
+    }
+}
+
+// (c - z) 2^-9 from a code operand
+constexpr float kExactScale8 = 32768.0f, kExactScale4 = 2048.0f;
+
+// The exponent by which scales up to `top` are taken so that they use fp16's range
+template <int BITS>
+__device__ __forceinline__ int scale_exponent(float top) {
+    const int e = (int)((__float_as_uint(top) >> 23) & 255u) - 126;  // top < 2^e
+    return min(max((BITS == 8 ? 15 : 11) - e, -126), 126);
+}
+
+// Tiles of row tile `rt` of a sequence; *base: the first tile's first token.
+template <int ROWS, int TILE>
+__device__ __forceinline__ int chunk_tiles(const KvqAttnArgs &a, const KvqSeq &s, int rt, int &base) {
+    const int rows = s.len * a.group;
+    const int t0 = rt * ROWS / a.group, t1 = (min(rows, (rt + 1) * ROWS) - 1) / a.group;
+    base = kvq_lo(a, s, t0) & ~(TILE - 1);
+    return max(1, (max(kvq_hi(s, t1) - base, 0) + TILE - 1) / TILE);
+}
+
+// A lane's outputs come in groups of four dimensions: register i_of of tile u_of holds
+// dimension dim_of + k of the lane's row.
+template <int D>
+struct ChunkOut {
+    static constexpr int kQuads = D / 8;
+    static __device__ __forceinline__ constexpr int u_of(int q, int k) {
+        return D == 64 ? k >> 1 : D == 128 ? k : 2 * k + (q >> 4);
+    }
+    static __device__ __forceinline__ constexpr int i_of(int q, int k) { return D == 64 ? q + 8 * (k & 1) : q & 15; }
+    static __device__ __forceinline__ int dim_of(int q, int half) {
+        return 4 * (32 * (q >> 4) + 8 * ((q & 15) >> 2) + 4 * half + (q & 3));
+    }
+};
+
+template <int GT>
+__device__ __forceinline__ void store_four(const KvqAttnArgs &a, int64_t row, int d, int dims, const float (&v)[4]) {
+    *reinterpret_cast<uint2 *>(a.out + row * dims + d) = make_uint2(round_pair<GT>(v[0], v[1]), round_pair<GT>(v[2], v[3]));
+}
+__device__ __forceinline__ int64_t out_row(const KvqAttnArgs &a, const KvqSeq &s, int g, int r) {
+    return (int64_t)(s.q0 + r / a.group) * a.q_heads + g * a.group + r % a.group;
+}
+__device__ __forceinline__ float lse_of(float m, float l) {
+    return l != 0.0f ? (m + log2f(l)) * 0.693147180559945f : -INFINITY;
+}
+
+template <int GT, int D, int BITS, int NW>
+__global__ __launch_bounds__(64 * NW, 2) void k_kvq_chunk(KvqAttnArgs a) {
+    using S = ChunkShape<GT, D, BITS, NW>;
+    constexpr bool kExact = S::kExact;
+    constexpr int kTile = S::kTile, kSub = S::kSub, kItems = S::kItems, kMTiles = D / 32, kSteps = D / 16;
+    constexpr int kOperandShift = kExact ? 9 : kCodeShift<BITS>;  // an operand is 2^-that of what it stands for
+    constexpr float kExactScale = BITS == 8 ? kExactScale8 : kExactScale4;
+    __shared__ _Float16 s_k[2][kTile][S::kKeyRow];
+    __shared__ _Float16 s_v[2][D][S::kValRow];
+    __shared__ float s_ks[2][kExact ? kTile : 1], s_vs[2][kExact ? kTile : 1];
+    __shared__ int64_t s_pre[kChunkSeqs + 1];
+    __shared__ int64_t s_scan[NW];
+    const int tid = threadIdx.x, lane = tid & 63, wave = uniform((int)(tid >> 6));
+    const int n = lane & 31, half = lane >> 5;
+
+    ChunkSplit *splits = reinterpret_cast<ChunkSplit *>(static_cast<char *>(a.workspace));
+    ChunkPartial<GT, D, NW> *parts =
+        reinterpret_cast<ChunkPartial<GT, D, NW> *>(static_cast<char *>(a.workspace) + kChunkMaxGroups * sizeof(ChunkSplit));
+
+    // ---- tiles of every sequence, as running sums
+    {
+        constexpr int kPer = (kChunkSeqs + S::kThreads - 1) / S::kThreads;
+        int64_t u[kPer], sum = 0;
+#pragma unroll
+        for (int k = 0; k < kPer; ++k) {
+            const int b = tid * kPer + k;
+            u[k] = 0;
+            if (b < a.batch) {
+                const KvqSeq s = kvq_seq(a, b);
+                const int64_t rows = (int64_t)s.len * a.group;
+                if (rows > a.max_rows)
+                    for (int rt = 0; rt * (int64_t)S::kRows < rows; ++rt) {
+                        int base;
+                        u[k] += chunk_tiles<S::kRows, kTile>(a, s, rt, base);
+                    }
+                u[k] *= a.c.heads;
+            }
+            sum += u[k];
+        }
+        int64_t incl = sum;
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) {
+            const int64_t t = __shfl_up(incl, d, 64);
+            if (lane >= d) incl += t;
+        }
+        if (lane == 63) s_scan[wave] = incl;
+        __syncthreads();
+        for (int w = 0; w < wave; ++w) incl += s_scan[w];
+        int64_t at = incl - sum;
+#pragma unroll
+        for (int k = 0; k < kPer; ++k) {
+            if (tid * kPer + k < kChunkSeqs) s_pre[tid * kPer + k] = at;
+            at += u[k];
+        }
+        if (tid == S::kThreads - 1) s_pre[kChunkSeqs] = at;
+        __syncthreads();
+    }
+    const int64_t total = uniform(s_pre[kChunkSeqs]);
+    const int64_t groups = min((int64_t)gridDim.x, total);
+    if (tid == 0) splits[blockIdx.x].last = -1;
+    if ((int64_t)blockIdx.x >= groups) return;
+    const int64_t each = udiv(total, groups), more = total - each * groups;
+    const auto begin_of = [&](int64_t w) { return w * each + min(w, more); };
+    const int64_t end = begin_of((int64_t)blockIdx.x + 1);
+    int64_t pos = begin_of(blockIdx.x);
+    int b;
+    {
+        int lo = 0, hi = kChunkSeqs;
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (s_pre[mid] <= pos) lo = mid; else hi = mid;
+        }
+        b = uniform(lo);
+    }
+
+    for (bool first = true; pos < end; first = false) {
+        while (s_pre[b + 1] <= pos) ++b;
+        b = uniform(b);
+        KvqSeq seq = kvq_seq(a, b);
+        seq.q0 = uniform(seq.q0);
+        seq.len = uniform(seq.len);
+        seq.kv = uniform(seq.kv);
+        int64_t off = pos - uniform(s_pre[b]);
+        int rt = 0, base, tiles;
+        for (;; ++rt) {
+            tiles = chunk_tiles<S::kRows, kTile>(a, seq, rt, base);
+            if (off < (int64_t)tiles * a.c.heads) break;
+            off -= (int64_t)tiles * a.c.heads;
+        }
+        const int g = uniform((int)off / tiles), u0 = uniform((int)off % tiles);
+        const int64_t item_begin = pos - u0, item_end = item_begin + tiles;
+        const int64_t seg_end = min(end, item_end);
+        const int r0 = rt * S::kRows, r1 = min(seq.len * a.group, r0 + S::kRows);
+        const int t0 = r0 / a.group, t1 = (r1 - 1) / a.group;
+        const int some_lo = kvq_lo(a, seq, t0), some_hi = kvq_hi(seq, t1);  // attended to by some row of the tile
+        // (an item that attends to nothing reads nothing: the cache may have no pages)
+        const int from = base + u0 * kTile, count = some_hi > base ? (int)(seg_end - pos) : 0;
+        const bool alone = pos == item_begin && seg_end == item_end;
+
+        // ---- this lane's query row
+        const int r = r0 + 32 * wave + n;
+        const bool live = r < r1;
+        const int my_t = live ? r / a.group : t1;
+        const int my_lo = kvq_lo(a, seq, my_t), my_hi = kvq_hi(seq, my_t);
+        // positions that all of the wave's rows attend to; a wave without rows only expands
+        const bool wave_live = r0 + 32 * wave < r1;
+        const int wt0 = (r0 + 32 * wave) / a.group, wt1 = (min(r1, r0 + 32 * wave + 32) - 1) / a.group;
+        const int all_lo = wave_live ? kvq_lo(a, seq, wt1) : 0, all_hi = wave_live ? kvq_hi(seq, wt0) : 0;
+        const int wave_lo = wave_live ? kvq_lo(a, seq, wt0) : 0, wave_hi = wave_live ? kvq_hi(seq, wt1) : 0;
+        f16x8_v qf[kSteps];
+        float qs;
+        {
+            const int h = live ? g * a.group + r % a.group : 0;
+            const uint16_t *src = a.q + (int64_t)(seq.q0 + my_t) * a.q_token_stride + (int64_t)h * a.q_head_stride;
+            uint4 raw[kSteps];
+#pragma unroll
+            for (int s = 0; s < kSteps; ++s)
+                raw[s] = live ? *reinterpret_cast<const uint4 *>(src + 16 * s + 8 * half) : make_uint4(0, 0, 0, 0);
+            float amax = 0.0f;
+#pragma unroll
+            for (int s = 0; s < kSteps; ++s) {
+                const uint32_t w[4] = {raw[s].x, raw[s].y, raw[s].z, raw[s].w};
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    amax = fmaxf(amax, fmaxf(fabsf(half_bits_to_float<GT>(w[k] & 0xffffu)),
+                                             fabsf(half_bits_to_float<GT>(w[k] >> 16))));
+            }
+            const int kq = query_exponent(fmaxf(amax, __shfl_xor(amax, 32, 64)));
+            const float up = __uint_as_float(__float_as_uint(pow2(kq)) ^ a.q_sign);
+#pragma unroll
+            for (int s = 0; s < kSteps; ++s) {
+                const uint32_t w[4] = {raw[s].x, raw[s].y, raw[s].z, raw[s].w};
+                float f[8];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    f[2 * k] = half_bits_to_float<GT>(w[k] & 0xffffu);
+                    f[2 * k + 1] = half_bits_to_float<GT>(w[k] >> 16);
+                }
+                qf[s] = query_operand<BITS>(f, up);
+            }
+            qs = ldexpf(a.scale2, kOperandShift - kq);
+            if (a.cap2 > 0.0f) qs *= a.cap_scale;
+        }
+
+        // ---- the tiles' way from the cache into LDS
+        const int32_t *table = a.table + (int64_t)b * a.table_stride;
+        const int last_page = a.max_tokens >> a.c.shift;
+        const auto page_of = [&](int j) -> int {
+            const int i = j >> a.c.shift;
+            return i < last_page ? table[i] : -1;
+        };
+        // cache row of token j; a page outside the cache gives rows of page 0, to be left out
+        const auto row_of = [&](int page, int j, bool &ok) -> int64_t {
+            ok = page >= 0 && page < a.c.n_pages && j >= some_lo && j < some_hi;
+            page = page >= 0 && page < a.c.n_pages ? page : 0;
+            return (int64_t)((((uint64_t)(uint32_t)page * (uint32_t)a.c.heads + (uint32_t)g) << a.c.shift) |
+                             (uint32_t)(j & (a.c.page - 1)));
+        };
+        uint32_t kw[kItems][S::kCodeWords], vw[kItems][4];
+        float kks[kItems], kvs[kItems];  // both scales of the piece's key row
+        float4 vvs[kItems];
+        bool k_ok[kItems], v_ok[kItems];
+        int k_page[kItems], v_page[kItems];
+        // piece i: 16 key dimensions of one token, and four value dimensions of four tokens
+        const auto key_token = [&](int i) { return (tid + i * S::kThreads) / (D / 16); };
+        const auto key_dim = [&](int i) { return 16 * ((tid + i * S::kThreads) % (D / 16)); };
+        const auto val_token = [&](int i) { return 4 * ((tid + i * S::kThreads) / (D / 4)); };
+        const auto val_dim = [&](int i) { return 4 * ((tid + i * S::kThreads) % (D / 4)); };
+        // tokens of the tile that lane `lane` watches the scales of (two rounds for 128 tokens)
+        constexpr int kWatch = kTile > 64 ? 2 : 1;
+        float w_ks[kWatch], w_vs[kWatch];
+        int w_page[kWatch];
+        bool w_ok[kWatch], w_there[kWatch];
+        uint64_t there[kWatch], there_next[kWatch];  // tokens whose pages are in the cache
+        const auto watch_token = [&](int i) { return (64 * i + lane) % kTile; };
+        const auto load_pages = [&](int j) {
+#pragma unroll
+            for (int i = 0; i < kItems; ++i) {
+                k_page[i] = page_of(j + key_token(i));
+                v_page[i] = page_of(j + val_token(i));
+            }
+#pragma unroll
+            for (int i = 0; i < kWatch; ++i) w_page[i] = page_of(j + watch_token(i));
+        };
+        const auto load_tile = [&](int j) {
+#pragma unroll
+            for (int i = 0; i < kItems; ++i) {
+                const int64_t kr = row_of(k_page[i], j + key_token(i), k_ok[i]);
+                kks[i] = a.c.scales[0][kr];
+                kvs[i] = a.c.scales[1][kr];
+                const uint8_t *p = a.c.codes[0] + kr * (D * BITS / 8) + key_dim(i) * BITS / 8;
+                if (BITS == 8) {
+                    const uint4 v = *reinterpret_cast<const uint4 *>(p);
+                    kw[i][0] = v.x; kw[i][1] = v.y; kw[i][2 % S::kCodeWords] = v.z; kw[i][3 % S::kCodeWords] = v.w;
+                } else {
+                    const uint2 v = *reinterpret_cast<const uint2 *>(p);
+                    kw[i][0] = v.x; kw[i][1] = v.y;
+                }
+                bool ok;
+                const int64_t vr = row_of(v_page[i], j + val_token(i), ok);
+                v_ok[i] = v_page[i] >= 0 && v_page[i] < a.c.n_pages;
+                vvs[i] = *reinterpret_cast<const float4 *>(a.c.scales[1] + vr);
+                const uint8_t *q = a.c.codes[1] + vr * (D * BITS / 8) + val_dim(i) * BITS / 8;
+#pragma unroll
+                for (int t = 0; t < 4; ++t)
+                    vw[i][t] = BITS == 8 ? *reinterpret_cast<const uint32_t *>(q + t * D)
+                                         : *reinterpret_cast<const uint16_t *>(q + t * (D / 2));
+            }
+#pragma unroll
+            for (int i = 0; i < kWatch; ++i) {
+                const int64_t wr = row_of(w_page[i], j + watch_token(i), w_ok[i]);
+                w_ks[i] = a.c.scales[0][wr];
+                w_vs[i] = a.c.scales[1][wr];
+                w_there[i] = w_page[i] >= 0 && w_page[i] < a.c.n_pages;
+            }
+        };
+        // exponents of the scales: of the tile in LDS, and of the one being expanded
+        float k_top = 0.0f, v_top = 0.0f;
+        int k_exp = 126, v_exp = 126, k_exp_next = 126, v_exp_next = 126;
+        const auto expand_tile = [&](int j, int buf) {
+            float kt = 0.0f, vt = 0.0f;
+#pragma unroll
+            for (int i = 0; i < kWatch; ++i) {
+                const float x = fabsf(w_ks[i]), y = fabsf(w_vs[i]);
+                const bool in = w_ok[i] && x < INFINITY && y < INFINITY;
+                there_next[i] = __ballot(w_there[i]);
+                kt = fmaxf(kt, in ? x : 0.0f);
+                vt = fmaxf(vt, in ? y : 0.0f);
+            }
+            if (__any(kt > k_top || vt > v_top)) {
+#pragma unroll
+                for (int d = 32; d >= 1; d >>= 1) {
+                    kt = fmaxf(kt, __shfl_xor(kt, d, 64));
+                    vt = fmaxf(vt, __shfl_xor(vt, d, 64));
+                }
+                k_top = fmaxf(k_top, kt);
+                v_top = fmaxf(v_top, vt);
+                k_exp_next = uniform(scale_exponent<BITS>(k_top));
+                v_exp_next = uniform(kExact ? value_exponent(v_top) : scale_exponent<BITS>(v_top));
+            }
+            const float kf = pow2(k_exp_next), vf = pow2(v_exp_next);
+#pragma unroll
+            for (int i = 0; i < kItems; ++i) {
+                // a scale that is not finite makes the scores of its token NaN and its values 0:
+                // NaN for the rows that attend to it, nothing for the others
+                const bool finite = fabsf(kks[i]) < INFINITY && fabsf(kvs[i]) < INFINITY;
+                const float ks = k_ok[i] ? (finite ? kks[i] : NAN) : 0.0f;
+                const f16x2_v scale = splat16(kExact ? kExactScale : ks * kf);
+                uint4 x[2];
+                expand16<BITS>(kw[i], scale, scale * (_Float16)-0x1p-17f, x);
+                uint4 *dst = reinterpret_cast<uint4 *>(&s_k[buf][key_token(i)][key_dim(i)]);
+                dst[0] = x[0];
+                dst[1] = x[1];
+                if (kExact && key_dim(i) == 0) {
+                    s_ks[buf][key_token(i)] = ks;
+                    s_vs[buf][key_token(i)] = k_ok[i] && finite ? kvs[i] * vf : 0.0f;
+                }
+                const float s4[4] = {vvs[i].x, vvs[i].y, vvs[i].z, vvs[i].w};
+                f16x2_v s2[2];
+#pragma unroll
+                for (int t = 0; t < 4; ++t) {
+                    const int at = j + val_token(i) + t;
+                    const bool in = v_ok[i] && at >= some_lo && at < some_hi && fabsf(s4[t]) < INFINITY;
+                    s2[t >> 1][t & 1] = (_Float16)(kExact ? kExactScale : in ? s4[t] * vf : 0.0f);
+                }
+                // four tokens are eight bytes; of each 16 tokens, those that one half of a wave
+                // multiplies lie together
+                const int quad = val_token(i) / 4;
+                const int to = 16 * (quad / 4) + 8 * (quad & 1) + 4 * ((quad >> 1) & 1);
+#pragma unroll
+                for (int d = 0; d < 4; ++d) {
+                    const uint32_t lo = fma16(code_pair<BITS>(vw[i][0], vw[i][1], d), s2[0], s2[0] * (_Float16)-0x1p-17f);
+                    const uint32_t hi = fma16(code_pair<BITS>(vw[i][2], vw[i][3], d), s2[1], s2[1] * (_Float16)-0x1p-17f);
+                    *reinterpret_cast<uint2 *>(&s_v[buf][d * (D / 4) + val_dim(i) / 4][to]) = make_uint2(lo, hi);
+                }
+            }
+        };
+
+        f32x16_v o[kMTiles];
+#pragma unroll
+        for (int u = 0; u < kMTiles; ++u)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) o[u][i] = 0.0f;
+        float m = -3.40282347e+38f, l = 0.0f;
+
+        if (count > 0) {
+            load_pages(from);
+            load_tile(from);
+        }
+        if (count > 1) load_pages(from + kTile);
+        __syncthreads();  // the item before is done with the buffers
+        if (count > 0) expand_tile(from, 0);
+        if (count > 1) load_tile(from + kTile);
+        if (count > 2) load_pages(from + 2 * kTile);
+        for (int it = 0; it < count; ++it) {
+            const int j = from + it * kTile, buf = it & 1;
+            if (v_exp != v_exp_next) {
+#pragma unroll
+                for (int u = 0; u < kMTiles; ++u)
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) o[u][i] = ldexpf(o[u][i], v_exp_next - v_exp);
+                v_exp = v_exp_next;
+            }
+            k_exp = k_exp_next;
+#pragma unroll
+            for (int i = 0; i < kWatch; ++i) there[i] = there_next[i];
+            __syncthreads();
+            if (it + 1 < count) {
+                expand_tile(j + kTile, buf ^ 1);
+                if (it + 2 < count) load_tile(j + 2 * kTile);
+                if (it + 3 < count) load_pages(j + 3 * kTile);
+            }
+            const float qk = kExact ? qs : ldexpf(qs, -k_exp);
+#pragma unroll
+            for (int sub = 0; sub < kTile / kSub; ++sub) {
+                const int js = j + sub * kSub;
+                if (js >= wave_hi || js + kSub <= wave_lo) continue;  // none of the wave's rows attends here
+                constexpr int kT = kSub / 32;
+                f32x16_v acc[kT];
+#pragma unroll
+                for (int tt = 0; tt < kT; ++tt) {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) acc[tt][i] = 0.0f;
+#pragma unroll
+                    for (int s = 0; s < kSteps; ++s) {
+                        const f16x8_v kf = *reinterpret_cast<const f16x8_v *>(
+                            &s_k[buf][sub * kSub + 32 * tt + n][16 * s + 8 * half]);
+                        acc[tt] = __builtin_amdgcn_mfma_f32_32x32x16_f16(kf, qf[s], acc[tt], 0, 0, 0);
+                    }
+                }
+                float scale = qk;
+                if (kExact) {
+#pragma unroll
+                    for (int tt = 0; tt < kT; ++tt)
+#pragma unroll
+                        for (int i = 0; i < 16; i += 4) {
+                            const float4 f =
+                                *reinterpret_cast<const float4 *>(&s_ks[buf][sub * kSub + 32 * tt + 2 * i + 4 * half]);
+                            acc[tt][i] *= f.x; acc[tt][i + 1] *= f.y; acc[tt][i + 2] *= f.z; acc[tt][i + 3] *= f.w;
+                        }
+                }
+                if (a.cap2 > 0.0f) {
+#pragma unroll
+                    for (int tt = 0; tt < kT; ++tt)
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) acc[tt][i] = capped(acc[tt][i] * qk, a.cap2);
+                    scale = 1.0f;
+                }
+                bool pages_ok = true;
+#pragma unroll
+                for (int i = 0; i < kWatch; ++i) pages_ok = pages_ok && there[i] == ~0ull;
+                const bool whole = js >= all_lo && js + kSub <= all_hi && pages_ok;
+                const auto attended = [&](int tt, int i) {
+                    const int at = sub * kSub + 32 * tt + 8 * (i / 4) + 4 * half + (i & 3);
+                    return j + at >= my_lo && j + at < my_hi && (pages_ok || (there[at / 64 % kWatch] >> (at & 63) & 1));
+                };
+                if (!whole) {
+#pragma unroll
+                    for (int tt = 0; tt < kT; ++tt)
+#pragma unroll
+                        for (int i = 0; i < 16; ++i)
+                            if (!attended(tt, i)) acc[tt][i] = -3.40282347e+38f;
+                }
+                float top = acc[0][0];
+#pragma unroll
+                for (int tt = 0; tt < kT; ++tt)
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) top = fmaxf(top, acc[tt][i]);
+                if (__any(top * scale > m + 8.0f)) {
+                    top = fmaxf(m, fmaxf(top, __shfl_xor(top, 32, 64)) * scale);
+                    const float f = exp2_fast(m - top);
+                    m = top;
+                    l *= f;
+#pragma unroll
+                    for (int u = 0; u < kMTiles; ++u)
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) o[u][i] *= f;
+                }
+                // weights relative to the running maximum, times 2^7: they use fp16's range
+                const float shift = kExact ? -m : 7.0f - m;
+                u32x4_v pw[kT][2], lw[kT][2];
+#pragma unroll
+                for (int tt = 0; tt < kT; ++tt)
+#pragma unroll
+                    for (int i = 0; i < 16; i += 4) {
+                        float e[4];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            e[k] = exp2_fast(fmaf(acc[tt][i + k], scale, shift));
+                            if (!whole) e[k] = attended(tt, i + k) ? e[k] : 0.0f;
+                        }
+                        if (kExact) {
+                            const float4 f =
+                                *reinterpret_cast<const float4 *>(&s_vs[buf][sub * kSub + 32 * tt + 2 * i + 4 * half]);
+                            l += (e[0] + e[1]) + (e[2] + e[3]);
+                            e[0] *= f.x; e[1] *= f.y; e[2] *= f.z; e[3] *= f.w;
+                        }
+#pragma unroll
+                        for (int k = 0; k < 4; k += 2) {
+                            const uint32_t p = round_pair<kGradF16>(e[k], e[k + 1]);
+                            pw[tt][i / 8][(i % 8) / 2 + k / 2] = p;
+                            if (kExact)
+                                lw[tt][i / 8][(i % 8) / 2 + k / 2] = rest_pair(e[k], e[k + 1], p);
+                            else
+                                l = add_pair(p, l);
+                        }
+                    }
+#pragma unroll
+                for (int tt = 0; tt < kT; ++tt)
+#pragma unroll
+                    for (int s = 0; s < 2; ++s)
+#pragma unroll
+                        for (int u = 0; u < kMTiles; ++u) {
+                            const f16x8_v vf = *reinterpret_cast<const f16x8_v *>(
+                                &s_v[buf][32 * u + n][sub * kSub + 32 * tt + 16 * s + 8 * half]);
+                            o[u] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vf, __builtin_bit_cast(f16x8_v, pw[tt][s]), o[u], 0, 0, 0);
+                            if (kExact)
+                                o[u] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vf, __builtin_bit_cast(f16x8_v, lw[tt][s]), o[u], 0, 0, 0);
+                        }
+            }
+        }
+
+        // ---- results
+        l += __shfl_xor(l, 32, 64);
+        const float inv = l != 0.0f ? 1.0f / l : 0.0f;
+        if (!kExact) l *= 0x1p-7f;
+#pragma unroll
+        for (int u = 0; u < kMTiles; ++u)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) o[u][i] = ldexpf(o[u][i] * inv, kOperandShift - v_exp);
+        if (alone) {
+            if (live) {
+                using O = ChunkOut<D>;
+                const int64_t to = out_row(a, seq, g, r);
+#pragma unroll
+                for (int q = 0; q < O::kQuads; ++q) {
+                    const float v[4] = {o[O::u_of(q, 0)][O::i_of(q, 0)], o[O::u_of(q, 1)][O::i_of(q, 1)],
+                                        o[O::u_of(q, 2)][O::i_of(q, 2)], o[O::u_of(q, 3)][O::i_of(q, 3)]};
+                    store_four<GT>(a, to, O::dim_of(q, half), D, v);
+                }
+                if (a.lse && half == 0) a.lse[to] = lse_of(m, l);
+            }
+        } else {
+            const int slot = 2 * blockIdx.x + (first ? 0 : 1);
+#pragma unroll
+            for (int u = 0; u < kMTiles; ++u)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) parts[slot].o[wave][16 * u + i][lane] = o[u][i];
+            if (half == 0) {
+                parts[slot].ml[wave][n][0] = m;
+                parts[slot].ml[wave][n][1] = l;
+            }
+            if (tid == 0 && pos == item_begin) {
+                const int64_t at = more * (each + 1), unit = item_end - 1;
+                ChunkSplit s{};
+                s.last = (int)(unit < at ? udiv(unit, each + 1) : more + udiv(unit - at, each));
+                s.slot = slot;
+                s.seq = b;
+                s.tile = rt;
+                s.head = g;
+                splits[blockIdx.x] = s;
+            }
+        }
+        pos = seg_end;
+    }
+}
+
+// Joins the parts of the item that workgroup blockIdx.x of k_kvq_chunk began and did
+// not end, for the rows of one of its waves.
+template <int GT, int D, int NW>
+__global__ __launch_bounds__(256) void k_kvq_chunk_join(KvqAttnArgs a) {
+    using O = ChunkOut<D>;
+    const ChunkSplit s = reinterpret_cast<const ChunkSplit *>(a.workspace)[blockIdx.x];
+    if (s.last < 0) return;
+    const ChunkPartial<GT, D, NW> *parts = reinterpret_cast<const ChunkPartial<GT, D, NW> *>(
+        static_cast<const char *>(a.workspace) + kChunkMaxGroups * sizeof(ChunkSplit));
+    const int lane = threadIdx.x & 63, share = threadIdx.x >> 6, wave = blockIdx.y;
+    const int n = lane & 31, half = lane >> 5;
+    const KvqSeq seq = kvq_seq(a, s.seq);
+    const int r = s.tile * 32 * NW + 32 * wave + n;
+    if (s.tile * 32 * NW + 32 * wave >= seq.len * a.group) return;
+    constexpr int kMine = O::kQuads / 4;
+    float v[kMine][4], m = -3.40282347e+38f, l = 0.0f;
+#pragma unroll
+    for (int q = 0; q < kMine; ++q)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) v[q][k] = 0.0f;
+    for (int w = blockIdx.x; w <= s.last; ++w) {
+        const ChunkPartial<GT, D, NW> &p = parts[w == (int)blockIdx.x ? s.slot : 2 * w];
+        const float pm = p.ml[wave][n][0], pl = p.ml[wave][n][1];
+        const float top = fmaxf(m, pm), f0 = exp2_fast(m - top), f = pl * exp2_fast(pm - top);
+        m = top;
+        l = l * f0 + f;
+#pragma unroll
+        for (int q = 0; q < kMine; ++q)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                // the register's number, with `share` the only part that is not a constant
+                const int at = kMine * share + q;
+                const int u = D == 64 ? k >> 1 : D == 128 ? k : 2 * k + (at >> 4);
+                const int i = D == 64 ? at + 8 * (k & 1) : at & 15;
+                v[q][k] = fmaf(p.o[wave][16 * u + i][lane], f, v[q][k] * f0);
+            }
+    }
+    const float inv = l != 0.0f ? 1.0f / l : 0.0f;
+    if (r >= seq.len * a.group) return;
+    const int64_t to = out_row(a, seq, s.head, r);
+#pragma unroll
+    for (int q = 0; q < kMine; ++q) {
+        const float x[4] = {v[q][0] * inv, v[q][1] * inv, v[q][2] * inv, v[q][3] * inv};
+        store_four<GT>(a, to, O::dim_of(kMine * share + q, half), D, x);
+    }
+    if (a.lse && share == 0 && half == 0) a.lse[to] = lse_of(m, l);
+}
+
+}  // namespace onebit

@@ -60,6 +60,10 @@ def attention(q, pools, table, kv_lens, *, bits, scale, q_offsets=None, softcap=
         by e: 2 e A;
       - the sums over n terms in fp32, of codes too: (n + 64) 2^-24 (A + R sum_j softmax_j scale_j),
         twice.
+    Chunks (more than 32 rows, tokens x heads of a cache head) of bf16 take the rows as fp16: the
+    scale and the product are each rounded once, 2^-10 of a key or value, and what fp16's range cuts
+    off is below 2^-14 of the largest scale: 2^-10 sum_d |q_d k_d| + 2^-14 max(scale) sum_d |q_d| for
+    a score, 2^-10 A + 2^-14 max(scale) for an output.
     Weights far below the row's largest lose bits to fp16's range: 2^-31 of the largest
     scale's row for each of the n terms.  lse is off by what the scores are, the sum's n roundings
     and its own (2^-22 of its size).
@@ -102,6 +106,11 @@ def attention(q, pools, table, kv_lens, *, bits, scale, q_offsets=None, softcap=
                 s = scale * (x @ k.T)
                 size = abs(scale) * reach * x.abs().sum(1, keepdim=True) * ks.double().abs()
                 off = (dim + 8) * 2.0 ** -24 * size + 2.0 ** -22 * (s.abs() + 1)
+                rounded = q.dtype == torch.bfloat16 and m * group > 32
+                k_top, v_top = (float(torch.nan_to_num(t, posinf=0.0).abs().max()) for t in (ks, vs))
+                if rounded:
+                    off = off + abs(scale) * (2.0 ** -10 * (x.abs() @ k.abs().T) +
+                                              2.0 ** -14 * k_top * x.abs().sum(1, keepdim=True))
                 if softcap:
                     s = softcap * torch.tanh(s / softcap)
                     off = off + 2.0 ** -21 * softcap
@@ -120,5 +129,5 @@ def attention(q, pools, table, kv_lens, *, bits, scale, q_offsets=None, softcap=
                 lse_tol[lo:hi, h] = (worst + (count + 64) * 2.0 ** -24).squeeze(1) + 2.0 ** -22 * (lse[lo:hi, h].abs() + 1)
                 wide = a + reach * (p @ vs.double().abs()).unsqueeze(1)
                 tol[lo:hi, h] = a * (2.0 ** -11 + 2 * worst) + 2 * (count + 64) * 2.0 ** -24 * wide + \
-                    count * 2.0 ** -31 * float(torch.nan_to_num(vs).max()) * top
+                    count * 2.0 ** -31 * v_top * top + (2.0 ** -10 * a + 2.0 ** -14 * v_top if rounded else 0.0)
     return out, lse, tol, lse_tol, owned

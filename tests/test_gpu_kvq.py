@@ -489,6 +489,19 @@ def test_empty_calls():
     assert (out == 0).all()
 
 
+@pytest.mark.parametrize("q_len", [1, 50])
+def test_a_cache_without_pages(q_len):
+    none = tuple(t.to(DEV) for t in empty_pools(0, 2, 16, 64, 8))
+    q = torch.ones(2 * q_len, 4, 64, dtype=BF16, device=DEV)
+    out, lse = torch.ones_like(q), torch.ones(2 * q_len, 4, device=DEV)
+    ws = torch.zeros(ob.kvq_attention_workspace_bytes(2, 2 * q_len, 4, 2, 64), dtype=torch.uint8, device=DEV)
+    table, lens = torch.zeros(2, 3, dtype=torch.int32, device=DEV), torch.full((2,), 40, dtype=torch.int32, device=DEV)
+    ob.kvq_attention(q, *none, table, lens, out, bits=8, lse=lse, workspace=ws)
+    assert (out == 0).all() and (lse == -math.inf).all()
+    ob.kvq_quantize(q[:, :2], q[:, 2:], torch.arange(2 * q_len, device=DEV), *none, bits=8)   # no slot exists
+    ob.kvq_dequantize(*none, torch.arange(2 * q_len, device=DEV), out[:, :2].contiguous(), out[:, 2:].contiguous(), bits=8)
+
+
 def test_rows_past_4_gib():
     """Codes and scales at byte offsets beyond 32 bits, written, read and attended to."""
     page, heads, dim = 1024, 8, 256
