@@ -10,6 +10,8 @@
 
 namespace onebit {
 
+constexpr int kChunkWaves = 8;
+
 static int compute_units() {
     int dev = 0, cus = 256;
     if (hipGetDevice(&dev) == hipSuccess) {
@@ -21,9 +23,8 @@ static int compute_units() {
 
 // Workgroups of a launch: as many as are resident at once.
 static int step_groups() { return std::min(3 * compute_units(), kStepMaxGroups); }
-static int chunk_groups() { return std::min(compute_units(), kChunkMaxGroups); }
+static int chunk_groups() { return std::min(8 / kChunkWaves * compute_units(), kChunkMaxGroups); }
 
-constexpr int kChunkWaves = 8;
 // The step kernel's counters, then the partial results of either kernel (one runs after
 // the other).
 static size_t step_bytes(int dim) {

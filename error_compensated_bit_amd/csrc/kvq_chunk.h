@@ -24,6 +24,7 @@
 
 namespace onebit {
 
+constexpr float kUnseen = -3.40282347e+38f;  // running maximum before the first key
 constexpr int kChunkSeqs = 512;        // sequences of one launch
 constexpr int kChunkMaxGroups = 1024;  // workgroups of one launch
 
@@ -46,13 +47,42 @@ struct ChunkShape {
     static constexpr bool kExact = GT == kGradF16;
     static constexpr int kThreads = 64 * NW, kRows = 32 * NW;
     static constexpr int kTile = D == 256 ? 32 : D == 128 ? 64 : 128;  // tokens
-    static constexpr int kSub = kTile < 64 ? kTile : 64;               // tokens of one softmax step
     static constexpr int kItems = kTile * D / 16 / kThreads;           // rows' pieces a thread expands
     static constexpr int kKeyRow = D + 8;                              // fp16 elements; 16 bytes of padding
     static constexpr int kValRow = kTile + 8;                          // spread the rows over the banks
     static constexpr int kCodeWords = BITS / 2;                        // words of 16 codes
     static_assert(kItems >= 1 && kItems * kThreads == kTile * D / 16, "every thread expands whole pieces");
 };
+
+// N products whose left operands come from LDS, kAhead reads in front, with the pieces
+// of some other work between them, in the order written: a product occupies the matrix
+// cores for 32 cycles, in which the wave can issue the other work's instructions, but
+// the compiler by itself puts every read right in front of its product and the other
+// work behind them all.
+constexpr int kAhead = 4;
+// A value that a piece computes for later: the compiler would move its computation there.
+__device__ __forceinline__ void pin(uint32_t &v) { asm volatile("" : "+v"(v)); }
+// The first reads are issued (read_first) well before the products they feed.
+template <int N, typename Read>
+__device__ __forceinline__ void read_first(f16x8_v (&f)[kAhead], Read read) {
+#pragma unroll
+    for (int x = 0; x < kAhead && x < N; ++x) f[x] = read(x);
+    __builtin_amdgcn_sched_barrier(0);
+}
+template <int N, int PIECES, typename Read, typename Product, typename Piece>
+__device__ __forceinline__ void weave(f16x8_v (&f)[kAhead], Read read, Product product, Piece piece) {
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int p = 0; p < PIECES; ++p) {
+#pragma unroll
+        for (int x = p * N / PIECES; x < (p + 1) * N / PIECES; ++x) {
+            product(x, f[x % kAhead]);
+            if (x + kAhead < N) f[x % kAhead] = read(x + kAhead);
+        }
+        piece(p);
+        __builtin_amdgcn_sched_barrier(0);
+    }
+}
 
 __device__ __forceinline__ f16x2_v splat16(float v) {
     const _Float16 h = (_Float16)v;
@@ -122,7 +152,7 @@ template <int GT, int D, int BITS, int NW>
 __global__ __launch_bounds__(64 * NW, 2) void k_kvq_chunk(KvqAttnArgs a) {
     using S = ChunkShape<GT, D, BITS, NW>;
     constexpr bool kExact = S::kExact;
-    constexpr int kTile = S::kTile, kSub = S::kSub, kItems = S::kItems, kMTiles = D / 32, kSteps = D / 16;
+    constexpr int kTile = S::kTile, kItems = S::kItems, kMTiles = D / 32, kSteps = D / 16;
     constexpr int kOperandShift = kExact ? 9 : kCodeShift<BITS>;  // an operand is 2^-that of what it stands for
     constexpr float kExactScale = BITS == 8 ? kExactScale8 : kExactScale4;
     __shared__ _Float16 s_k[2][kTile][S::kKeyRow];
@@ -264,86 +294,95 @@ __global__ __launch_bounds__(64 * NW, 2) void k_kvq_chunk(KvqAttnArgs a) {
 
         // ---- the tiles' way from the cache into LDS
         const int32_t *table = a.table + (int64_t)b * a.table_stride;
-        const int last_page = a.max_tokens >> a.c.shift;
-        const auto page_of = [&](int j) -> int {
-            const int i = j >> a.c.shift;
-            return i < last_page ? table[i] : -1;
-        };
-        // cache row of token j; a page outside the cache gives rows of page 0, to be left out
-        const auto row_of = [&](int page, int j, bool &ok) -> int64_t {
-            ok = page >= 0 && page < a.c.n_pages && j >= some_lo && j < some_hi;
-            page = page >= 0 && page < a.c.n_pages ? page : 0;
-            return (int64_t)((((uint64_t)(uint32_t)page * (uint32_t)a.c.heads + (uint32_t)g) << a.c.shift) |
+        // Page number of token j.  No branch, here or in row_of: the compiler would wait for
+        // all loads under way where the ways join.  Tokens behind the table's end get its last page
+        // (they are behind the sequence's end too, and so masked); a page outside the cache gives
+        // rows of page 0, to be left out.
+        const int last_page = (a.max_tokens >> a.c.shift) - 1;
+        const uint32_t pages = (uint32_t)min(a.c.n_pages, (int64_t)1 << 31);
+        const auto page_of = [&](int j) -> int { return table[min(j >> a.c.shift, last_page)]; };
+        const auto there_is = [&](int page) { return (uint32_t)page < pages; };
+        const auto row_of = [&](int page, int j) -> int64_t {
+            return (int64_t)((((uint64_t)(uint32_t)(there_is(page) ? page : 0) * (uint32_t)a.c.heads + (uint32_t)g)
+                              << a.c.shift) |
                              (uint32_t)(j & (a.c.page - 1)));
         };
+        // Piece i of a thread: 16 key dimensions of one token, and four value dimensions of four
+        // tokens.  A wave's pieces are of kWaveTokens consecutive tokens, in one page.
+        constexpr int kWaveTokens = 1024 / D, kRowBytes = D * BITS / 8;
+        const auto first_token = [&](int i) { return (wave + i * NW) * kWaveTokens; };
+        const int k_token = lane / (D / 16), k_dim = 16 * (lane % (D / 16));
+        const int v_token = 4 * (lane / (D / 4)), v_dim = 4 * (lane % (D / 4));
         uint32_t kw[kItems][S::kCodeWords], vw[kItems][4];
         float kks[kItems], kvs[kItems];  // both scales of the piece's key row
         float4 vvs[kItems];
-        bool k_ok[kItems], v_ok[kItems];
-        int k_page[kItems], v_page[kItems];
-        // piece i: 16 key dimensions of one token, and four value dimensions of four tokens
-        const auto key_token = [&](int i) { return (tid + i * S::kThreads) / (D / 16); };
-        const auto key_dim = [&](int i) { return 16 * ((tid + i * S::kThreads) % (D / 16)); };
-        const auto val_token = [&](int i) { return 4 * ((tid + i * S::kThreads) / (D / 4)); };
-        const auto val_dim = [&](int i) { return 4 * ((tid + i * S::kThreads) % (D / 4)); };
-        // tokens of the tile that lane `lane` watches the scales of (two rounds for 128 tokens)
+        int page[kItems], page_here[kItems];
+        // tokens of the tile that a lane watches the scales of (two rounds for 128 tokens)
         constexpr int kWatch = kTile > 64 ? 2 : 1;
         float w_ks[kWatch], w_vs[kWatch];
-        int w_page[kWatch];
+        int w_page[kWatch], w_page_here[kWatch];
         bool w_ok[kWatch], w_there[kWatch];
         uint64_t there[kWatch], there_next[kWatch];  // tokens whose pages are in the cache
         const auto watch_token = [&](int i) { return (64 * i + lane) % kTile; };
         const auto load_pages = [&](int j) {
 #pragma unroll
-            for (int i = 0; i < kItems; ++i) {
-                k_page[i] = page_of(j + key_token(i));
-                v_page[i] = page_of(j + val_token(i));
-            }
+            for (int i = 0; i < kItems; ++i) page[i] = page_of(j + first_token(i));
 #pragma unroll
             for (int i = 0; i < kWatch; ++i) w_page[i] = page_of(j + watch_token(i));
+        };
+        // the pages loaded last are the next tile's
+        const auto take_pages = [&]() {
+#pragma unroll
+            for (int i = 0; i < kItems; ++i) page_here[i] = uniform(page[i]);
+#pragma unroll
+            for (int i = 0; i < kWatch; ++i) w_page_here[i] = w_page[i];
         };
         const auto load_tile = [&](int j) {
 #pragma unroll
             for (int i = 0; i < kItems; ++i) {
-                const int64_t kr = row_of(k_page[i], j + key_token(i), k_ok[i]);
-                kks[i] = a.c.scales[0][kr];
-                kvs[i] = a.c.scales[1][kr];
-                const uint8_t *p = a.c.codes[0] + kr * (D * BITS / 8) + key_dim(i) * BITS / 8;
+                const int64_t row = row_of(page_here[i], j + first_token(i));
+                const uint8_t *kp = a.c.codes[0] + row * kRowBytes, *vp = a.c.codes[1] + row * kRowBytes;
+                const float *ksp = a.c.scales[0] + row, *vsp = a.c.scales[1] + row;
+                kks[i] = ksp[k_token];
+                kvs[i] = vsp[k_token];
+                vvs[i] = *reinterpret_cast<const float4 *>(vsp + v_token);
+                kp += k_token * kRowBytes + k_dim * BITS / 8;
                 if (BITS == 8) {
-                    const uint4 v = *reinterpret_cast<const uint4 *>(p);
+                    const uint4 v = *reinterpret_cast<const uint4 *>(kp);
                     kw[i][0] = v.x; kw[i][1] = v.y; kw[i][2 % S::kCodeWords] = v.z; kw[i][3 % S::kCodeWords] = v.w;
                 } else {
-                    const uint2 v = *reinterpret_cast<const uint2 *>(p);
+                    const uint2 v = *reinterpret_cast<const uint2 *>(kp);
                     kw[i][0] = v.x; kw[i][1] = v.y;
                 }
-                bool ok;
-                const int64_t vr = row_of(v_page[i], j + val_token(i), ok);
-                v_ok[i] = v_page[i] >= 0 && v_page[i] < a.c.n_pages;
-                vvs[i] = *reinterpret_cast<const float4 *>(a.c.scales[1] + vr);
-                const uint8_t *q = a.c.codes[1] + vr * (D * BITS / 8) + val_dim(i) * BITS / 8;
+                vp += v_token * kRowBytes + v_dim * BITS / 8;
 #pragma unroll
                 for (int t = 0; t < 4; ++t)
-                    vw[i][t] = BITS == 8 ? *reinterpret_cast<const uint32_t *>(q + t * D)
-                                         : *reinterpret_cast<const uint16_t *>(q + t * (D / 2));
+                    vw[i][t] = BITS == 8 ? *reinterpret_cast<const uint32_t *>(vp + t * kRowBytes)
+                                         : *reinterpret_cast<const uint16_t *>(vp + t * kRowBytes);
             }
 #pragma unroll
             for (int i = 0; i < kWatch; ++i) {
-                const int64_t wr = row_of(w_page[i], j + watch_token(i), w_ok[i]);
+                const int at = j + watch_token(i);
+                const int64_t wr = row_of(w_page_here[i], at);
                 w_ks[i] = a.c.scales[0][wr];
                 w_vs[i] = a.c.scales[1][wr];
-                w_there[i] = w_page[i] >= 0 && w_page[i] < a.c.n_pages;
+                w_there[i] = there_is(w_page_here[i]);
+                w_ok[i] = w_there[i] & (at >= some_lo) & (at < some_hi);
             }
         };
         // exponents of the scales: of the tile in LDS, and of the one being expanded
         float k_top = 0.0f, v_top = 0.0f;
         int k_exp = 126, v_exp = 126, k_exp_next = 126, v_exp_next = 126;
-        const auto expand_tile = [&](int j, int buf) {
+        float x_ks[kItems], x_kv[kItems], x_s4[kItems][4], kf, vf;
+        const auto expand_begin = [&](int j) {
             float kt = 0.0f, vt = 0.0f;
+            bool plain = true;  // every token is attended to by some row and has finite scales
 #pragma unroll
             for (int i = 0; i < kWatch; ++i) {
                 const float x = fabsf(w_ks[i]), y = fabsf(w_vs[i]);
                 const bool in = w_ok[i] && x < INFINITY && y < INFINITY;
                 there_next[i] = __ballot(w_there[i]);
+                plain = plain && __ballot(in) == ~0ull;
                 kt = fmaxf(kt, in ? x : 0.0f);
                 vt = fmaxf(vt, in ? y : 0.0f);
             }
@@ -358,41 +397,58 @@ __global__ __launch_bounds__(64 * NW, 2) void k_kvq_chunk(KvqAttnArgs a) {
                 k_exp_next = uniform(scale_exponent<BITS>(k_top));
                 v_exp_next = uniform(kExact ? value_exponent(v_top) : scale_exponent<BITS>(v_top));
             }
-            const float kf = pow2(k_exp_next), vf = pow2(v_exp_next);
+            kf = pow2(k_exp_next);
+            vf = pow2(v_exp_next);
 #pragma unroll
             for (int i = 0; i < kItems; ++i) {
-                // a scale that is not finite makes the scores of its token NaN and its values 0:
-                // NaN for the rows that attend to it, nothing for the others
-                const bool finite = fabsf(kks[i]) < INFINITY && fabsf(kvs[i]) < INFINITY;
-                const float ks = k_ok[i] ? (finite ? kks[i] : NAN) : 0.0f;
-                const f16x2_v scale = splat16(kExact ? kExactScale : ks * kf);
+                float ks = kks[i], kv = kvs[i], s4[4] = {vvs[i].x, vvs[i].y, vvs[i].z, vvs[i].w};
+                if (!plain) {
+                    // a scale that is not finite makes the scores of its token NaN and its values 0: NaN
+                    // for the rows that attend to it, nothing for the others
+                    const bool ok = there_is(page_here[i]);
+                    const int at = j + first_token(i) + k_token;
+                    const bool in = ok && at >= some_lo && at < some_hi;
+                    const bool finite = fabsf(ks) < INFINITY && fabsf(kv) < INFINITY;
+                    ks = in ? (finite ? ks : NAN) : 0.0f;
+                    kv = in && finite ? kv : 0.0f;
+#pragma unroll
+                    for (int t = 0; t < 4; ++t) {
+                        const int vat = j + first_token(i) + v_token + t;
+                        s4[t] = ok && vat >= some_lo && vat < some_hi && fabsf(s4[t]) < INFINITY ? s4[t] : 0.0f;
+                    }
+                }
+                x_ks[i] = ks;
+                x_kv[i] = kv;
+#pragma unroll
+                for (int t = 0; t < 4; ++t) x_s4[i][t] = s4[t];
+            }
+        };
+        // the expansion in pieces: the keys' row, then a dimension of the values at a time
+        constexpr int kPieces = 5 * kItems;
+        const auto expand_piece = [&](int buf, int piece) {
+            const int i = piece / 5, d = piece % 5 - 1;
+            if (d < 0) {
+                const f16x2_v scale = splat16(kExact ? kExactScale : x_ks[i] * kf);
                 uint4 x[2];
                 expand16<BITS>(kw[i], scale, scale * (_Float16)-0x1p-17f, x);
-                uint4 *dst = reinterpret_cast<uint4 *>(&s_k[buf][key_token(i)][key_dim(i)]);
+                uint4 *dst = reinterpret_cast<uint4 *>(&s_k[buf][first_token(i) + k_token][k_dim]);
                 dst[0] = x[0];
                 dst[1] = x[1];
-                if (kExact && key_dim(i) == 0) {
-                    s_ks[buf][key_token(i)] = ks;
-                    s_vs[buf][key_token(i)] = k_ok[i] && finite ? kvs[i] * vf : 0.0f;
+                if (kExact && k_dim == 0) {
+                    s_ks[buf][first_token(i) + k_token] = x_ks[i];
+                    s_vs[buf][first_token(i) + k_token] = x_kv[i] * vf;
                 }
-                const float s4[4] = {vvs[i].x, vvs[i].y, vvs[i].z, vvs[i].w};
+            } else {
                 f16x2_v s2[2];
 #pragma unroll
-                for (int t = 0; t < 4; ++t) {
-                    const int at = j + val_token(i) + t;
-                    const bool in = v_ok[i] && at >= some_lo && at < some_hi && fabsf(s4[t]) < INFINITY;
-                    s2[t >> 1][t & 1] = (_Float16)(kExact ? kExactScale : in ? s4[t] * vf : 0.0f);
-                }
+                for (int t = 0; t < 4; ++t) s2[t >> 1][t & 1] = (_Float16)(kExact ? kExactScale : x_s4[i][t] * vf);
                 // four tokens are eight bytes; of each 16 tokens, those that one half of a wave
                 // multiplies lie together
-                const int quad = val_token(i) / 4;
+                const int quad = (first_token(i) + v_token) / 4;
                 const int to = 16 * (quad / 4) + 8 * (quad & 1) + 4 * ((quad >> 1) & 1);
-#pragma unroll
-                for (int d = 0; d < 4; ++d) {
-                    const uint32_t lo = fma16(code_pair<BITS>(vw[i][0], vw[i][1], d), s2[0], s2[0] * (_Float16)-0x1p-17f);
-                    const uint32_t hi = fma16(code_pair<BITS>(vw[i][2], vw[i][3], d), s2[1], s2[1] * (_Float16)-0x1p-17f);
-                    *reinterpret_cast<uint2 *>(&s_v[buf][d * (D / 4) + val_dim(i) / 4][to]) = make_uint2(lo, hi);
-                }
+                const uint32_t lo = fma16(code_pair<BITS>(vw[i][0], vw[i][1], d), s2[0], s2[0] * (_Float16)-0x1p-17f);
+                const uint32_t hi = fma16(code_pair<BITS>(vw[i][2], vw[i][3], d), s2[1], s2[1] * (_Float16)-0x1p-17f);
+                *reinterpret_cast<uint2 *>(&s_v[buf][d * (D / 4) + v_dim / 4][to]) = make_uint2(lo, hi);
             }
         };
 
@@ -401,17 +457,26 @@ __global__ __launch_bounds__(64 * NW, 2) void k_kvq_chunk(KvqAttnArgs a) {
         for (int u = 0; u < kMTiles; ++u)
 #pragma unroll
             for (int i = 0; i < 16; ++i) o[u][i] = 0.0f;
-        float m = -3.40282347e+38f, l = 0.0f;
+        float m = kUnseen, l = 0.0f;
 
+        // (loads past the last tile are of rows that exist and are not used)
         if (count > 0) {
             load_pages(from);
+            take_pages();
+            load_pages(from + kTile);
             load_tile(from);
         }
-        if (count > 1) load_pages(from + kTile);
         __syncthreads();  // the item before is done with the buffers
-        if (count > 0) expand_tile(from, 0);
-        if (count > 1) load_tile(from + kTile);
-        if (count > 2) load_pages(from + 2 * kTile);
+        if (count > 0) {
+            expand_begin(from);
+#pragma unroll
+            for (int x = 0; x < kPieces; ++x) expand_piece(0, x);
+        }
+        if (count > 0) {
+            take_pages();
+            load_pages(from + 2 * kTile);
+            load_tile(from + kTile);
+        }
         for (int it = 0; it < count; ++it) {
             const int j = from + it * kTile, buf = it & 1;
             if (v_exp != v_exp_next) {
@@ -425,119 +490,155 @@ __global__ __launch_bounds__(64 * NW, 2) void k_kvq_chunk(KvqAttnArgs a) {
 #pragma unroll
             for (int i = 0; i < kWatch; ++i) there[i] = there_next[i];
             __syncthreads();
-            if (it + 1 < count) {
-                expand_tile(j + kTile, buf ^ 1);
-                if (it + 2 < count) load_tile(j + 2 * kTile);
-                if (it + 3 < count) load_pages(j + 3 * kTile);
+            // the wave's rows attend to some of the tile, or the wave only expands
+            const bool active = j < wave_hi && j + kTile > wave_lo, more_tiles = it + 1 < count;
+            constexpr int kSubs = kTile / 32, kPv = 2 * kMTiles;
+            f32x16_v acc[2];
+            const auto read_k = [&](int sub, int x) {
+                return *reinterpret_cast<const f16x8_v *>(&s_k[buf][32 * sub + n][16 * x + 8 * half]);
+            };
+            const auto mul_k = [&](int sub, int x, f16x8_v f) {
+                acc[sub & 1] = __builtin_amdgcn_mfma_f32_32x32x16_f16(f, qf[x], acc[sub & 1], 0, 0, 0);
+            };
+            const auto clear = [&](int sub) {
+#pragma unroll
+                for (int i = 0; i < 16; ++i) acc[sub & 1][i] = 0.0f;
+            };
+            f16x8_v ahead[kAhead];
+            const auto read_k0 = [&](int x) { return read_k(0, x); };
+            const auto mul_k0 = [&](int x, f16x8_v f) { mul_k(0, x, f); };
+            if (active) read_first<kSteps>(ahead, read_k0);
+            if (more_tiles) expand_begin(j + kTile);
+            if (active && more_tiles) {
+                clear(0);
+                weave<kSteps, kPieces>(ahead, read_k0, mul_k0, [&](int x) { expand_piece(buf ^ 1, x); });
+            } else if (active) {
+                clear(0);
+                weave<kSteps, 1>(ahead, read_k0, mul_k0, [](int) {});
+            } else if (more_tiles) {
+#pragma unroll
+                for (int x = 0; x < kPieces; ++x) expand_piece(buf ^ 1, x);
             }
-            const float qk = kExact ? qs : ldexpf(qs, -k_exp);
+            take_pages();
+            load_pages(j + 3 * kTile);
+            load_tile(j + 2 * kTile);
+            if (!active) continue;
+
+            // 32 tokens at a time: while their weights are computed, the matrix cores multiply the
+            // next ones' scores and the last ones' values
+            // (kept above 0, so that the weight of a score of -inf, a key not attended to, is 0)
+            const float qk = fmaxf(kExact ? qs : ldexpf(qs, -k_exp), 0x1p-126f);
+            u32x4_v pw[2][2], lw[2][2];  // weights of two such steps, each for two products of 16 tokens
+            const auto read_v = [&](int sub, int x) {
+                return *reinterpret_cast<const f16x8_v *>(
+                    &s_v[buf][32 * (x % kMTiles) + n][32 * sub + 16 * (x / kMTiles) + 8 * half]);
+            };
+            const auto mul_v = [&](int sub, int x, f16x8_v f) {
+                const int u = x % kMTiles, t = x / kMTiles;
+                o[u] = __builtin_amdgcn_mfma_f32_32x32x16_f16(f, __builtin_bit_cast(f16x8_v, pw[sub & 1][t]), o[u], 0, 0, 0);
+                if (kExact)
+                    o[u] = __builtin_amdgcn_mfma_f32_32x32x16_f16(f, __builtin_bit_cast(f16x8_v, lw[sub & 1][t]), o[u], 0, 0, 0);
+            };
 #pragma unroll
-            for (int sub = 0; sub < kTile / kSub; ++sub) {
-                const int js = j + sub * kSub;
-                if (js >= wave_hi || js + kSub <= wave_lo) continue;  // none of the wave's rows attends here
-                constexpr int kT = kSub / 32;
-                f32x16_v acc[kT];
-#pragma unroll
-                for (int tt = 0; tt < kT; ++tt) {
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) acc[tt][i] = 0.0f;
-#pragma unroll
-                    for (int s = 0; s < kSteps; ++s) {
-                        const f16x8_v kf = *reinterpret_cast<const f16x8_v *>(
-                            &s_k[buf][sub * kSub + 32 * tt + n][16 * s + 8 * half]);
-                        acc[tt] = __builtin_amdgcn_mfma_f32_32x32x16_f16(kf, qf[s], acc[tt], 0, 0, 0);
-                    }
-                }
+            for (int sub = 0; sub < kSubs; ++sub) {
+                f32x16_v &x = acc[sub & 1];
+                const int js = j + 32 * sub;
+                constexpr int kBoth = kSteps + kPv;
+                const bool next = sub + 1 < kSubs, last = sub > 0;  // there are next scores, last values
+                const auto read_both = [&](int i) { return i < kSteps ? read_k(sub + 1, i) : read_v(sub - 1, i - kSteps); };
+                const auto mul_both = [&](int i, f16x8_v g) {
+                    if (i < kSteps) mul_k(sub + 1, i, g); else mul_v(sub - 1, i - kSteps, g);
+                };
+                const auto read_next = [&](int i) { return read_k(sub + 1, i); };
+                const auto mul_next = [&](int i, f16x8_v g) { mul_k(sub + 1, i, g); };
+                const auto read_last = [&](int i) { return read_v(sub - 1, i); };
+                const auto mul_last = [&](int i, f16x8_v g) { mul_v(sub - 1, i, g); };
+                if (next && last)
+                    read_first<kBoth>(ahead, read_both);
+                else if (next)
+                    read_first<kSteps>(ahead, read_next);
+                else if (last)
+                    read_first<kPv>(ahead, read_last);
                 float scale = qk;
                 if (kExact) {
 #pragma unroll
-                    for (int tt = 0; tt < kT; ++tt)
-#pragma unroll
-                        for (int i = 0; i < 16; i += 4) {
-                            const float4 f =
-                                *reinterpret_cast<const float4 *>(&s_ks[buf][sub * kSub + 32 * tt + 2 * i + 4 * half]);
-                            acc[tt][i] *= f.x; acc[tt][i + 1] *= f.y; acc[tt][i + 2] *= f.z; acc[tt][i + 3] *= f.w;
-                        }
+                    for (int i = 0; i < 16; i += 4) {
+                        const float4 f = *reinterpret_cast<const float4 *>(&s_ks[buf][32 * sub + 2 * i + 4 * half]);
+                        x[i] *= f.x; x[i + 1] *= f.y; x[i + 2] *= f.z; x[i + 3] *= f.w;
+                    }
                 }
                 if (a.cap2 > 0.0f) {
 #pragma unroll
-                    for (int tt = 0; tt < kT; ++tt)
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) acc[tt][i] = capped(acc[tt][i] * qk, a.cap2);
+                    for (int i = 0; i < 16; ++i) x[i] = capped(x[i] * qk, a.cap2);
                     scale = 1.0f;
                 }
-                bool pages_ok = true;
-#pragma unroll
-                for (int i = 0; i < kWatch; ++i) pages_ok = pages_ok && there[i] == ~0ull;
-                const bool whole = js >= all_lo && js + kSub <= all_hi && pages_ok;
-                const auto attended = [&](int tt, int i) {
-                    const int at = sub * kSub + 32 * tt + 8 * (i / 4) + 4 * half + (i & 3);
-                    return j + at >= my_lo && j + at < my_hi && (pages_ok || (there[at / 64 % kWatch] >> (at & 63) & 1));
-                };
+                const uint32_t here = (uint32_t)(there[sub / 2] >> (32 * (sub & 1)));
+                const bool whole = js >= all_lo && js + 32 <= all_hi && here == ~0u;
                 if (!whole) {
+                    // the tokens that this lane's row attends to, one bit each, from its half's first
+                    const int lo = min(max(my_lo - js, 0), 32), hi = min(max(my_hi - js, 0), 32);
+                    const uint64_t bits = ((1ull << hi) - 1) & ~((1ull << lo) - 1) & here;
+                    const uint32_t mine = (uint32_t)(bits >> (4 * half));
 #pragma unroll
-                    for (int tt = 0; tt < kT; ++tt)
-#pragma unroll
-                        for (int i = 0; i < 16; ++i)
-                            if (!attended(tt, i)) acc[tt][i] = -3.40282347e+38f;
+                    for (int i = 0; i < 16; ++i)
+                        if (!(mine >> (8 * (i / 4) + (i & 3)) & 1)) x[i] = -INFINITY;
                 }
-                float top = acc[0][0];
+                float top = x[0];
 #pragma unroll
-                for (int tt = 0; tt < kT; ++tt)
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) top = fmaxf(top, acc[tt][i]);
-                if (__any(top * scale > m + 8.0f)) {
+                for (int i = 1; i < 16; ++i) top = fmaxf(top, x[i]);
+                const bool grow = __any(top * scale > m + 8.0f);
+                float f = 1.0f;  // what the sums so far are to be multiplied by
+                if (grow) {
                     top = fmaxf(m, fmaxf(top, __shfl_xor(top, 32, 64)) * scale);
-                    const float f = exp2_fast(m - top);
+                    f = exp2_fast(m - top);
                     m = top;
                     l *= f;
+                }
+                // weights relative to the running maximum, times 2^7: they use fp16's range
+                const float shift = kExact ? -m : 7.0f - m;
+                const auto weigh = [&](int q) {  // two pairs of tokens
+                    const int i = 2 * q;
+                    float e[2];
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) e[k] = exp2_fast(fmaf(x[i + k], scale, shift));
+                    l += e[0] + e[1];
+                    if (kExact) {
+                        const float2 v = *reinterpret_cast<const float2 *>(
+                            &s_vs[buf][32 * sub + 8 * (i / 4) + 4 * half + (i & 3)]);
+                        e[0] *= v.x;
+                        e[1] *= v.y;
+                    }
+                    uint32_t p = round_pair<kGradF16>(e[0], e[1]), rest = 0;
+                    if (kExact) {
+                        rest = rest_pair(e[0], e[1], p);
+                        pin(rest);
+                        lw[sub & 1][i / 8][(i % 8) / 2] = rest;
+                    }
+                    pin(p);
+                    pw[sub & 1][i / 8][(i % 8) / 2] = p;
+                };
+                if (next) clear(sub + 1);
+                if (next && last) {
+                    weave<kBoth, 8>(ahead, read_both, mul_both, weigh);
+                } else if (next) {
+                    weave<kSteps, 8>(ahead, read_next, mul_next, weigh);
+                } else if (last) {
+                    weave<kPv, 8>(ahead, read_last, mul_last, weigh);
+                } else {
+#pragma unroll
+                    for (int q = 0; q < 8; ++q) weigh(q);
+                }
+                if (!next) read_first<kPv>(ahead, [&](int i) { return read_v(sub, i); });
+                // (the last step's values went in with weights relative to the maximum before this one)
+                if (grow) {
 #pragma unroll
                     for (int u = 0; u < kMTiles; ++u)
 #pragma unroll
                         for (int i = 0; i < 16; ++i) o[u][i] *= f;
                 }
-                // weights relative to the running maximum, times 2^7: they use fp16's range
-                const float shift = kExact ? -m : 7.0f - m;
-                u32x4_v pw[kT][2], lw[kT][2];
-#pragma unroll
-                for (int tt = 0; tt < kT; ++tt)
-#pragma unroll
-                    for (int i = 0; i < 16; i += 4) {
-                        float e[4];
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            e[k] = exp2_fast(fmaf(acc[tt][i + k], scale, shift));
-                            if (!whole) e[k] = attended(tt, i + k) ? e[k] : 0.0f;
-                        }
-                        if (kExact) {
-                            const float4 f =
-                                *reinterpret_cast<const float4 *>(&s_vs[buf][sub * kSub + 32 * tt + 2 * i + 4 * half]);
-                            l += (e[0] + e[1]) + (e[2] + e[3]);
-                            e[0] *= f.x; e[1] *= f.y; e[2] *= f.z; e[3] *= f.w;
-                        }
-#pragma unroll
-                        for (int k = 0; k < 4; k += 2) {
-                            const uint32_t p = round_pair<kGradF16>(e[k], e[k + 1]);
-                            pw[tt][i / 8][(i % 8) / 2 + k / 2] = p;
-                            if (kExact)
-                                lw[tt][i / 8][(i % 8) / 2 + k / 2] = rest_pair(e[k], e[k + 1], p);
-                            else
-                                l = add_pair(p, l);
-                        }
-                    }
-#pragma unroll
-                for (int tt = 0; tt < kT; ++tt)
-#pragma unroll
-                    for (int s = 0; s < 2; ++s)
-#pragma unroll
-                        for (int u = 0; u < kMTiles; ++u) {
-                            const f16x8_v vf = *reinterpret_cast<const f16x8_v *>(
-                                &s_v[buf][32 * u + n][sub * kSub + 32 * tt + 16 * s + 8 * half]);
-                            o[u] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vf, __builtin_bit_cast(f16x8_v, pw[tt][s]), o[u], 0, 0, 0);
-                            if (kExact)
-                                o[u] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vf, __builtin_bit_cast(f16x8_v, lw[tt][s]), o[u], 0, 0, 0);
-                        }
             }
+            weave<kPv, 1>(ahead, [&](int x) { return read_v(kSubs - 1, x); },
+                          [&](int x, f16x8_v g) { mul_v(kSubs - 1, x, g); }, [](int) {});
         }
 
         // ---- results
@@ -600,7 +701,7 @@ __global__ __launch_bounds__(256) void k_kvq_chunk_join(KvqAttnArgs a) {
     const int r = s.tile * 32 * NW + 32 * wave + n;
     if (s.tile * 32 * NW + 32 * wave >= seq.len * a.group) return;
     constexpr int kMine = O::kQuads / 4;
-    float v[kMine][4], m = -3.40282347e+38f, l = 0.0f;
+    float v[kMine][4], m = kUnseen, l = 0.0f;
 #pragma unroll
     for (int q = 0; q < kMine; ++q)
 #pragma unroll

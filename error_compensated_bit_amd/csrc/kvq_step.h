@@ -271,17 +271,18 @@ __global__ __launch_bounds__(kStepBlock, NT == 1 && D <= 128 ? 3 : 2) void k_kvq
         int kv_exp = 126;                    // value scales are taken times 2^kv_exp
         float v_top = 0.0f;                  // the largest the exponent was chosen for
         const int32_t *table = a.table + (int64_t)b * a.table_stride;
-        const int last_page = a.max_tokens >> a.c.shift;
-        // page number of token j, and the cache row of token j (a multiple of 16); a page
-        // outside the cache gives rows of page 0, which are then left out
-        const auto page_of = [&](int j) -> int {
-            const int i = j >> a.c.shift;
-            return i < last_page ? table[i] : -1;
-        };
+        // page number of token j, and the cache row of token j (a multiple of 16); without branches,
+        // where the compiler would wait for all loads under way.  Tokens behind the table's end
+        // get its last page (they are masked); a page outside the cache gives rows of page 0, to be
+        // left out.
+        const int last_page = (a.max_tokens >> a.c.shift) - 1;
+        const uint32_t in_cache = (uint32_t)min(a.c.n_pages, (int64_t)1 << 31);
+        const auto page_of = [&](int j) -> int { return table[min(j >> a.c.shift, last_page)]; };
         const auto row_of = [&](int page, int j, bool &ok) -> int64_t {
             page = uniform(page);
-            ok = page >= 0 && page < a.c.n_pages;
-            return ((int64_t)(ok ? page : 0) * a.c.heads + g) * a.c.page + (j & (a.c.page - 1));
+            ok = (uint32_t)page < in_cache;
+            return (int64_t)((((uint64_t)(uint32_t)(ok ? page : 0) * (uint32_t)a.c.heads + (uint32_t)g) << a.c.shift) |
+                             (uint32_t)(j & (a.c.page - 1)));
         };
         uint32_t kw[2][T::kPieces * T::kPieceWords], vw[2][4][T::kValWords];
         float4 ks[2];
@@ -323,16 +324,16 @@ __global__ __launch_bounds__(kStepBlock, NT == 1 && D <= 128 ? 3 : 2) void k_kvq
             const bool whole = j >= all_lo && j + 32 <= all_hi && ok[0] && ok[1];
             const bool page_ok[2] = {ok[0], ok[1]};
             const float kscale[2][4] = {{ks[0].x, ks[0].y, ks[0].z, ks[0].w}, {ks[1].x, ks[1].y, ks[1].z, ks[1].w}};
-            // the next tile's keys are on their way from here on
-            if (j + kStepUnit < to) {
+            // the next tile's keys are on their way from here on (behind the last tile: of rows
+            // that exist and are not used)
 #pragma unroll
-                for (int tt = 0; tt < 2; ++tt) {
-                    row[tt] = row_of(pages[tt], j + kStepUnit + 16 * tt, ok[tt]);
-                    T::load_keys(a.c.codes[0] + row[tt] * T::kRow, lane, kw[tt]);
-                    ks[tt] = *reinterpret_cast<const float4 *>(a.c.scales[0] + row[tt] + 4 * c);
-                }
+            for (int tt = 0; tt < 2; ++tt) row[tt] = row_of(pages[tt], j + kStepUnit + 16 * tt, ok[tt]);
 #pragma unroll
-                for (int tt = 0; tt < 2; ++tt) pages[tt] = page_of(j + 2 * kStepUnit + 16 * tt);
+            for (int tt = 0; tt < 2; ++tt) pages[tt] = page_of(j + 2 * kStepUnit + 16 * tt);
+#pragma unroll
+            for (int tt = 0; tt < 2; ++tt) {
+                T::load_keys(a.c.codes[0] + row[tt] * T::kRow, lane, kw[tt]);
+                ks[tt] = *reinterpret_cast<const float4 *>(a.c.scales[0] + row[tt] + 4 * c);
             }
             // scores in units of log2(e)
             float x[NT][8];
