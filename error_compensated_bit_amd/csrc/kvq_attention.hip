@@ -10,8 +10,6 @@
 
 namespace onebit {
 
-constexpr int kChunkWaves = 8;
-
 static int compute_units() {
     int dev = 0, cus = 256;
     if (hipGetDevice(&dev) == hipSuccess) {
@@ -23,7 +21,10 @@ static int compute_units() {
 
 // Workgroups of a launch: as many as are resident at once.
 static int step_groups() { return std::min(3 * compute_units(), kStepMaxGroups); }
-static int chunk_groups() { return std::min(8 / kChunkWaves * compute_units(), kChunkMaxGroups); }
+static int chunk_groups() { return std::min(compute_units(), kChunkMaxGroups); }
+// Waves of a chunk workgroup.  With 256 dimensions a wave's outputs, queries and scores
+// need more than half of a SIMD's registers, so there is room for one on each.
+constexpr int chunk_waves(int dim) { return dim == 256 ? 4 : 8; }
 
 // The step kernel's counters, then the partial results of either kernel (one runs after
 // the other).
@@ -32,7 +33,7 @@ static size_t step_bytes(int dim) {
 }
 static size_t chunk_bytes(int dim) {
     return kChunkMaxGroups * sizeof(ChunkSplit) +
-           (size_t)chunk_groups() * 2 * kChunkWaves * 32 * (dim + 2) * sizeof(float);
+           (size_t)chunk_groups() * 2 * chunk_waves(dim) * 32 * (dim + 2) * sizeof(float);
 }
 
 static size_t attention_workspace(int64_t batch, int64_t total_q, int q_heads, int kv_heads, int head_dim) {
@@ -55,7 +56,7 @@ static KvqAttnArgs slice(const KvqAttnArgs &a, int b, int count) {
 
 template <int GT, int D, int BITS>
 static void launch(KvqAttnArgs a, hipStream_t s) {
-    constexpr int kWide = D == 256 ? 1 : 2;
+    constexpr int kWide = D == 256 ? 1 : 2, kWaves = chunk_waves(D);
     a.max_rows = 32;
     const int64_t rows = (int64_t)a.q_uniform * a.group;  // of every sequence, where that is known
     if (a.q_offsets || rows <= a.max_rows) {
@@ -73,8 +74,8 @@ static void launch(KvqAttnArgs a, hipStream_t s) {
         for (int b = 0; b < a.batch; b += kChunkSeqs) {
             KvqAttnArgs x = slice(a, b, kChunkSeqs);
             x.workspace = static_cast<char *>(a.workspace) + kStepHeader;
-            hipLaunchKernelGGL((k_kvq_chunk<GT, D, BITS, kChunkWaves>), dim3(chunk_groups()), dim3(64 * kChunkWaves), 0, s, x);
-            hipLaunchKernelGGL((k_kvq_chunk_join<GT, D, kChunkWaves>), dim3(chunk_groups(), kChunkWaves), dim3(256), 0, s, x);
+            hipLaunchKernelGGL((k_kvq_chunk<GT, D, BITS, kWaves>), dim3(chunk_groups()), dim3(64 * kWaves), 0, s, x);
+            hipLaunchKernelGGL((k_kvq_chunk_join<GT, D, kWaves>), dim3(chunk_groups(), kWaves), dim3(256), 0, s, x);
         }
     }
 }

@@ -63,6 +63,12 @@ constexpr int kAhead = 4;
 // A value that a piece computes for later: the compiler would move its computation there.
 __device__ __forceinline__ void pin(uint32_t &v) { asm volatile("" : "+v"(v)); }
 // The first reads are issued (read_first) well before the products they feed.
+// The largest of three, NaN if one is: one instruction, where fmaxf costs one more for
+// each operand that might be a signalling NaN.  (A row with a NaN score comes out NaN
+// whatever its running maximum.)
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    return __builtin_elementwise_maximum(__builtin_elementwise_maximum(a, b), c);
+}
 template <int N, typename Read>
 __device__ __forceinline__ void read_first(f16x8_v (&f)[kAhead], Read read) {
 #pragma unroll
@@ -149,15 +155,15 @@ __device__ __forceinline__ float lse_of(float m, float l) {
 }
 
 template <int GT, int D, int BITS, int NW>
-__global__ __launch_bounds__(64 * NW, 2) void k_kvq_chunk(KvqAttnArgs a) {
+__global__ __launch_bounds__(64 * NW, NW / 4) void k_kvq_chunk(KvqAttnArgs a) {
     using S = ChunkShape<GT, D, BITS, NW>;
     constexpr bool kExact = S::kExact;
     constexpr int kTile = S::kTile, kItems = S::kItems, kMTiles = D / 32, kSteps = D / 16;
     constexpr int kOperandShift = kExact ? 9 : kCodeShift<BITS>;  // an operand is 2^-that of what it stands for
     constexpr float kExactScale = BITS == 8 ? kExactScale8 : kExactScale4;
-    __shared__ _Float16 s_k[2][kTile][S::kKeyRow];
-    __shared__ _Float16 s_v[2][D][S::kValRow];
-    __shared__ float s_ks[2][kExact ? kTile : 1], s_vs[2][kExact ? kTile : 1];
+    __shared__ _Float16 s_k[4][kTile][S::kKeyRow];
+    __shared__ _Float16 s_v[4][D][S::kValRow];
+    __shared__ float s_ks[4][kExact ? kTile : 1], s_vs[4][kExact ? kTile : 1];
     __shared__ int64_t s_pre[kChunkSeqs + 1];
     __shared__ int64_t s_scan[NW];
     const int tid = threadIdx.x, lane = tid & 63, wave = uniform((int)(tid >> 6));
@@ -256,7 +262,6 @@ __global__ __launch_bounds__(64 * NW, 2) void k_kvq_chunk(KvqAttnArgs a) {
         const bool wave_live = r0 + 32 * wave < r1;
         const int wt0 = (r0 + 32 * wave) / a.group, wt1 = (min(r1, r0 + 32 * wave + 32) - 1) / a.group;
         const int all_lo = wave_live ? kvq_lo(a, seq, wt1) : 0, all_hi = wave_live ? kvq_hi(seq, wt0) : 0;
-        const int wave_lo = wave_live ? kvq_lo(a, seq, wt0) : 0, wave_hi = wave_live ? kvq_hi(seq, wt1) : 0;
         f16x8_v qf[kSteps];
         float qs;
         {
@@ -322,7 +327,7 @@ __global__ __launch_bounds__(64 * NW, 2) void k_kvq_chunk(KvqAttnArgs a) {
         float w_ks[kWatch], w_vs[kWatch];
         int w_page[kWatch], w_page_here[kWatch];
         bool w_ok[kWatch], w_there[kWatch];
-        uint64_t there[kWatch], there_next[kWatch];  // tokens whose pages are in the cache
+        uint64_t there_next[kWatch];  // tokens whose pages are in the cache
         const auto watch_token = [&](int i) { return (64 * i + lane) % kTile; };
         const auto load_pages = [&](int j) {
 #pragma unroll
@@ -372,7 +377,7 @@ __global__ __launch_bounds__(64 * NW, 2) void k_kvq_chunk(KvqAttnArgs a) {
         };
         // exponents of the scales: of the tile in LDS, and of the one being expanded
         float k_top = 0.0f, v_top = 0.0f;
-        int k_exp = 126, v_exp = 126, k_exp_next = 126, v_exp_next = 126;
+        int k_exp_next = 126, v_exp_next = 126;
         float x_ks[kItems], x_kv[kItems], x_s4[kItems][4], kf, vf;
         const auto expand_begin = [&](int j) {
             float kt = 0.0f, vt = 0.0f;
@@ -452,128 +457,57 @@ __global__ __launch_bounds__(64 * NW, 2) void k_kvq_chunk(KvqAttnArgs a) {
             }
         };
 
-        f32x16_v o[kMTiles];
+        constexpr int kSubs = kTile / 32, kPv = 2 * kMTiles;
+        f32x16_v o[kMTiles], acc[2];  // outputs; scores of this step and the next
+        u32x4_v pw[2][2], lw[2][2];   // weights of this step and the last, each for two products of 16 tokens
+        float m = kUnseen, l = 0.0f;
+        float f_grow = 1.0f, scale = 0.0f;
+        bool grow = false;
+        int v_exp = 126;                       // of what the outputs have summed
+        int k_exps[3], v_exps[3];              // of tiles it, it + 1, it + 2
+        uint64_t theres[2][kWatch];            // of tiles it, it + 1
 #pragma unroll
         for (int u = 0; u < kMTiles; ++u)
 #pragma unroll
             for (int i = 0; i < 16; ++i) o[u][i] = 0.0f;
-        float m = kUnseen, l = 0.0f;
-
-        // (loads past the last tile are of rows that exist and are not used)
-        if (count > 0) {
-            load_pages(from);
-            take_pages();
-            load_pages(from + kTile);
-            load_tile(from);
-        }
-        __syncthreads();  // the item before is done with the buffers
-        if (count > 0) {
-            expand_begin(from);
 #pragma unroll
-            for (int x = 0; x < kPieces; ++x) expand_piece(0, x);
-        }
-        if (count > 0) {
-            take_pages();
-            load_pages(from + 2 * kTile);
-            load_tile(from + kTile);
-        }
-        for (int it = 0; it < count; ++it) {
-            const int j = from + it * kTile, buf = it & 1;
-            if (v_exp != v_exp_next) {
+        for (int t = 0; t < 2; ++t)
 #pragma unroll
-                for (int u = 0; u < kMTiles; ++u)
+            for (int k = 0; k < 2; ++k) pw[t][k] = lw[t][k] = (u32x4_v){0u, 0u, 0u, 0u};
+        const auto read_k = [&](int buf, int sub, int x) {
+            return *reinterpret_cast<const f16x8_v *>(&s_k[buf][32 * sub + n][16 * x + 8 * half]);
+        };
+        const auto read_v = [&](int buf, int sub, int x) {
+            return *reinterpret_cast<const f16x8_v *>(
+                &s_v[buf][32 * (x % kMTiles) + n][32 * sub + 16 * (x / kMTiles) + 8 * half]);
+        };
+        const auto mul_k = [&](f32x16_v &to, int x, f16x8_v f) {
+            to = __builtin_amdgcn_mfma_f32_32x32x16_f16(f, qf[x], to, 0, 0, 0);
+        };
+        const auto mul_v = [&](int w, int x, f16x8_v f) {
+            const int u = x % kMTiles, t = x / kMTiles;
+            o[u] = __builtin_amdgcn_mfma_f32_32x32x16_f16(f, __builtin_bit_cast(f16x8_v, pw[w][t]), o[u], 0, 0, 0);
+            if (kExact)
+                o[u] = __builtin_amdgcn_mfma_f32_32x32x16_f16(f, __builtin_bit_cast(f16x8_v, lw[w][t]), o[u], 0, 0, 0);
+        };
+        const auto clear = [](f32x16_v &x) {
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) o[u][i] = ldexpf(o[u][i], v_exp_next - v_exp);
-                v_exp = v_exp_next;
-            }
-            k_exp = k_exp_next;
-#pragma unroll
-            for (int i = 0; i < kWatch; ++i) there[i] = there_next[i];
-            __syncthreads();
-            // the wave's rows attend to some of the tile, or the wave only expands
-            const bool active = j < wave_hi && j + kTile > wave_lo, more_tiles = it + 1 < count;
-            constexpr int kSubs = kTile / 32, kPv = 2 * kMTiles;
-            f32x16_v acc[2];
-            const auto read_k = [&](int sub, int x) {
-                return *reinterpret_cast<const f16x8_v *>(&s_k[buf][32 * sub + n][16 * x + 8 * half]);
-            };
-            const auto mul_k = [&](int sub, int x, f16x8_v f) {
-                acc[sub & 1] = __builtin_amdgcn_mfma_f32_32x32x16_f16(f, qf[x], acc[sub & 1], 0, 0, 0);
-            };
-            const auto clear = [&](int sub) {
-#pragma unroll
-                for (int i = 0; i < 16; ++i) acc[sub & 1][i] = 0.0f;
-            };
-            f16x8_v ahead[kAhead];
-            const auto read_k0 = [&](int x) { return read_k(0, x); };
-            const auto mul_k0 = [&](int x, f16x8_v f) { mul_k(0, x, f); };
-            if (active) read_first<kSteps>(ahead, read_k0);
-            if (more_tiles) expand_begin(j + kTile);
-            if (active && more_tiles) {
-                clear(0);
-                weave<kSteps, kPieces>(ahead, read_k0, mul_k0, [&](int x) { expand_piece(buf ^ 1, x); });
-            } else if (active) {
-                clear(0);
-                weave<kSteps, 1>(ahead, read_k0, mul_k0, [](int) {});
-            } else if (more_tiles) {
-#pragma unroll
-                for (int x = 0; x < kPieces; ++x) expand_piece(buf ^ 1, x);
-            }
-            take_pages();
-            load_pages(j + 3 * kTile);
-            load_tile(j + 2 * kTile);
-            if (!active) continue;
-
-            // 32 tokens at a time: while their weights are computed, the matrix cores multiply the
-            // next ones' scores and the last ones' values
+            for (int i = 0; i < 16; ++i) x[i] = 0.0f;
+        };
+        // scores of step `sub` of the tile in `buf`, whose first token is js: scales, cap and mask,
+        // and the running maximum.  `top` is the row's largest raw score where that is all there is to do.
+        const auto settle = [&](f32x16_v &x, float top, int buf, int sub, int js, int k_exp, const uint64_t (&here2)[kWatch]) {
             // (kept above 0, so that the weight of a score of -inf, a key not attended to, is 0)
             const float qk = fmaxf(kExact ? qs : ldexpf(qs, -k_exp), 0x1p-126f);
-            u32x4_v pw[2][2], lw[2][2];  // weights of two such steps, each for two products of 16 tokens
-            const auto read_v = [&](int sub, int x) {
-                return *reinterpret_cast<const f16x8_v *>(
-                    &s_v[buf][32 * (x % kMTiles) + n][32 * sub + 16 * (x / kMTiles) + 8 * half]);
-            };
-            const auto mul_v = [&](int sub, int x, f16x8_v f) {
-                const int u = x % kMTiles, t = x / kMTiles;
-                o[u] = __builtin_amdgcn_mfma_f32_32x32x16_f16(f, __builtin_bit_cast(f16x8_v, pw[sub & 1][t]), o[u], 0, 0, 0);
-                if (kExact)
-                    o[u] = __builtin_amdgcn_mfma_f32_32x32x16_f16(f, __builtin_bit_cast(f16x8_v, lw[sub & 1][t]), o[u], 0, 0, 0);
-            };
-#pragma unroll
-            for (int sub = 0; sub < kSubs; ++sub) {
-                f32x16_v &x = acc[sub & 1];
-                const int js = j + 32 * sub;
-                constexpr int kBoth = kSteps + kPv;
-                const bool next = sub + 1 < kSubs, last = sub > 0;  // there are next scores, last values
-                const auto read_both = [&](int i) { return i < kSteps ? read_k(sub + 1, i) : read_v(sub - 1, i - kSteps); };
-                const auto mul_both = [&](int i, f16x8_v g) {
-                    if (i < kSteps) mul_k(sub + 1, i, g); else mul_v(sub - 1, i - kSteps, g);
-                };
-                const auto read_next = [&](int i) { return read_k(sub + 1, i); };
-                const auto mul_next = [&](int i, f16x8_v g) { mul_k(sub + 1, i, g); };
-                const auto read_last = [&](int i) { return read_v(sub - 1, i); };
-                const auto mul_last = [&](int i, f16x8_v g) { mul_v(sub - 1, i, g); };
-                if (next && last)
-                    read_first<kBoth>(ahead, read_both);
-                else if (next)
-                    read_first<kSteps>(ahead, read_next);
-                else if (last)
-                    read_first<kPv>(ahead, read_last);
-                float scale = qk;
-                if (kExact) {
-#pragma unroll
-                    for (int i = 0; i < 16; i += 4) {
-                        const float4 f = *reinterpret_cast<const float4 *>(&s_ks[buf][32 * sub + 2 * i + 4 * half]);
-                        x[i] *= f.x; x[i + 1] *= f.y; x[i + 2] *= f.z; x[i + 3] *= f.w;
-                    }
-                }
+            const uint32_t here = (uint32_t)(here2[sub / 2] >> (32 * (sub & 1)));
+            const bool whole = js >= all_lo && js + 32 <= all_hi && here == ~0u;
+            scale = qk;
+            if (a.cap2 > 0.0f || !whole) {
                 if (a.cap2 > 0.0f) {
 #pragma unroll
                     for (int i = 0; i < 16; ++i) x[i] = capped(x[i] * qk, a.cap2);
                     scale = 1.0f;
                 }
-                const uint32_t here = (uint32_t)(there[sub / 2] >> (32 * (sub & 1)));
-                const bool whole = js >= all_lo && js + 32 <= all_hi && here == ~0u;
                 if (!whole) {
                     // the tokens that this lane's row attends to, one bit each, from its half's first
                     const int lo = min(max(my_lo - js, 0), 32), hi = min(max(my_hi - js, 0), 32);
@@ -583,24 +517,102 @@ __global__ __launch_bounds__(64 * NW, 2) void k_kvq_chunk(KvqAttnArgs a) {
                     for (int i = 0; i < 16; ++i)
                         if (!(mine >> (8 * (i / 4) + (i & 3)) & 1)) x[i] = -INFINITY;
                 }
-                float top = x[0];
+                top = x[0];
 #pragma unroll
-                for (int i = 1; i < 16; ++i) top = fmaxf(top, x[i]);
-                const bool grow = __any(top * scale > m + 8.0f);
-                float f = 1.0f;  // what the sums so far are to be multiplied by
-                if (grow) {
-                    top = fmaxf(m, fmaxf(top, __shfl_xor(top, 32, 64)) * scale);
-                    f = exp2_fast(m - top);
-                    m = top;
-                    l *= f;
+                for (int i = 0; i < 16; i += 2) top = max3(top, x[i], x[i + 1]);
+            }
+            grow = __any(top * scale > m + 8.0f);
+            if (grow) {
+                top = fmaxf(m, fmaxf(top, __shfl_xor(top, 32, 64)) * scale);
+                f_grow = exp2_fast(m - top);
+                m = top;
+                l *= f_grow;
+            }
+        };
+        // fp16 outputs: the key scales, applied to the scores in fp32
+        const auto scale_keys = [&](f32x16_v &x, int buf, int sub, int i) {
+            const float4 f = *reinterpret_cast<const float4 *>(&s_ks[buf][32 * sub + 2 * i + 4 * half]);
+            x[i] *= f.x; x[i + 1] *= f.y; x[i + 2] *= f.z; x[i + 3] *= f.w;
+        };
+
+        if (count > 0) {
+            // two tiles in LDS and the third on its way.  (Loads past the last tile are of rows that
+            // exist; what is made of them is not used.)
+            load_pages(from);
+            take_pages();
+            load_pages(from + kTile);
+            load_tile(from);
+            __syncthreads();  // the item before is done with the buffers
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                expand_begin(from + t * kTile);
+#pragma unroll
+                for (int x = 0; x < kPieces; ++x) expand_piece(t, x);
+                k_exps[t] = k_exp_next;
+                v_exps[t] = v_exp_next;
+#pragma unroll
+                for (int i = 0; i < kWatch; ++i) theres[t][i] = there_next[i];
+                take_pages();
+                load_pages(from + (t + 2) * kTile);
+                load_tile(from + (t + 1) * kTile);
+            }
+            v_exp = v_exps[0];
+            __syncthreads();
+            if (wave_live) {
+                clear(acc[0]);
+#pragma unroll
+                for (int x = 0; x < kSteps; ++x) mul_k(acc[0], x, read_k(0, 0, x));
+                if (kExact) {
+#pragma unroll
+                    for (int i = 0; i < 16; i += 4) scale_keys(acc[0], 0, 0, i);
                 }
+                float top = acc[0][0];
+#pragma unroll
+                for (int i = 0; i < 16; i += 2) top = max3(top, acc[0][i], acc[0][i + 1]);
+                settle(acc[0], top, 0, 0, from, k_exps[0], theres[0]);
+            }
+        }
+        // A step is 32 tokens.  While its weights are computed, the matrix cores multiply the next
+        // step's scores and the last step's values; in a tile's first step the tile after next is
+        // expanded, too.  Four tiles' places in LDS: the one before this, whose last values are
+        // still to be multiplied, this and the next one, and the one being expanded.
+        for (int it = 0; it < count; ++it) {
+            const int j = from + it * kTile, buf = it & 3, after = (it + 1) & 3, fresh = (it + 2) & 3;
+            if (it > 0) __syncthreads();
+            if (!wave_live) {
+                expand_begin(j + 2 * kTile);
+#pragma unroll
+                for (int x = 0; x < kPieces; ++x) expand_piece(fresh, x);
+                take_pages();
+                load_pages(j + 4 * kTile);
+                load_tile(j + 3 * kTile);
+                continue;
+            }
+#pragma unroll
+            for (int sub = 0; sub < kSubs; ++sub) {
+                const int cur = kSubs == 1 ? 0 : sub & 1, nxt = cur ^ 1;
+                const bool wrap = sub + 1 == kSubs;  // the next step is the next tile's first
+                const int kb = wrap ? after : buf, ks = wrap ? 0 : sub + 1;
+                // (before the first step there are no last values: weights of 0, and any finite values)
+                const int vb = sub ? buf : it ? (it - 1) & 3 : 0, vs = sub ? sub - 1 : kSubs - 1;
+                constexpr int kN = kSteps + kPv;
+                const auto read = [&](int x) { return x < kSteps ? read_k(kb, ks, x) : read_v(vb, vs, x - kSteps); };
+                f16x8_v ahead[kAhead];
+                read_first<kN>(ahead, read);
+                if (sub == 0) {
+                    expand_begin(j + 2 * kTile);
+                    k_exps[2] = k_exp_next;
+                    v_exps[2] = v_exp_next;
+                }
+                f32x16_v &x = acc[cur], &y = acc[nxt];
+                clear(y);
                 // weights relative to the running maximum, times 2^7: they use fp16's range
-                const float shift = kExact ? -m : 7.0f - m;
-                const auto weigh = [&](int q) {  // two pairs of tokens
+                const float shift = kExact ? -m : 7.0f - m, by = scale;
+                const auto weigh = [&](int q) {  // of two tokens
                     const int i = 2 * q;
                     float e[2];
 #pragma unroll
-                    for (int k = 0; k < 2; ++k) e[k] = exp2_fast(fmaf(x[i + k], scale, shift));
+                    for (int k = 0; k < 2; ++k) e[k] = exp2_fast(fmaf(x[i + k], by, shift));
                     l += e[0] + e[1];
                     if (kExact) {
                         const float2 v = *reinterpret_cast<const float2 *>(
@@ -612,33 +624,78 @@ __global__ __launch_bounds__(64 * NW, 2) void k_kvq_chunk(KvqAttnArgs a) {
                     if (kExact) {
                         rest = rest_pair(e[0], e[1], p);
                         pin(rest);
-                        lw[sub & 1][i / 8][(i % 8) / 2] = rest;
+                        lw[cur][i / 8][(i % 8) / 2] = rest;
                     }
                     pin(p);
-                    pw[sub & 1][i / 8][(i % 8) / 2] = p;
+                    pw[cur][i / 8][(i % 8) / 2] = p;
                 };
-                if (next) clear(sub + 1);
-                if (next && last) {
-                    weave<kBoth, 8>(ahead, read_both, mul_both, weigh);
-                } else if (next) {
-                    weave<kSteps, 8>(ahead, read_next, mul_next, weigh);
-                } else if (last) {
-                    weave<kPv, 8>(ahead, read_last, mul_last, weigh);
-                } else {
-#pragma unroll
-                    for (int q = 0; q < 8; ++q) weigh(q);
-                }
-                if (!next) read_first<kPv>(ahead, [&](int i) { return read_v(sub, i); });
-                // (the last step's values went in with weights relative to the maximum before this one)
+                float top = kUnseen;
+                const auto largest = [&](int i) {  // of four of the next scores
+                    if (kExact) scale_keys(y, kb, ks, i);
+                    top = max3(max3(top, y[i], y[i + 1]), y[i + 2], y[i + 3]);
+                };
+                constexpr int kFirst = kPieces + 1;  // pieces of a tile's first step more than of the others
+                const auto piece = [&](int p) {
+                    if (sub > 0) p += kFirst;
+                    if (p < kPieces)
+                        expand_piece(fresh, p);
+                    else if (p < kFirst) {
+                        take_pages();
+                        load_pages(j + 4 * kTile);
+                        load_tile(j + 3 * kTile);
+                    } else if (p < kFirst + 8)
+                        weigh(p - kFirst);
+                    else
+                        largest(4 * (p - kFirst - 8));
+                };
+                const auto product = [&](int x, f16x8_v g) { if (x < kSteps) mul_k(y, x, g); else mul_v(nxt, x - kSteps, g); };
+                if (sub == 0)
+                    weave<kN, kFirst + 12>(ahead, read, product, piece);
+                else
+                    weave<kN, 12>(ahead, read, product, piece);
+                // (the last values went in with weights relative to the maximum before this step's,
+                // and with the scales' exponent of their own tile)
                 if (grow) {
 #pragma unroll
                     for (int u = 0; u < kMTiles; ++u)
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) o[u][i] *= f;
+                        for (int i = 0; i < 16; ++i) o[u][i] *= f_grow;
+                }
+                if (sub == 0 && v_exp != v_exps[0]) {
+#pragma unroll
+                    for (int u = 0; u < kMTiles; ++u)
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) o[u][i] = ldexpf(o[u][i], v_exps[0] - v_exp);
+                    v_exp = v_exps[0];
+                }
+                if (wrap) {
+                    k_exps[0] = k_exps[1];
+                    k_exps[1] = k_exps[2];
+                    v_exps[0] = v_exps[1];
+                    v_exps[1] = v_exps[2];
+#pragma unroll
+                    for (int i = 0; i < kWatch; ++i) {
+                        theres[0][i] = theres[1][i];
+                        theres[1][i] = there_next[i];
+                    }
+                }
+                grow = false;
+                if (!wrap || it + 1 < count) settle(y, top, kb, ks, wrap ? j + kTile : j + 32 * (sub + 1), k_exps[0], theres[0]);
+                if (kSubs == 1) {
+                    x = y;
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        pw[1][k] = pw[0][k];
+                        lw[1][k] = lw[0][k];
+                    }
                 }
             }
-            weave<kPv, 1>(ahead, [&](int x) { return read_v(kSubs - 1, x); },
-                          [&](int x, f16x8_v g) { mul_v(kSubs - 1, x, g); }, [](int) {});
+        }
+        if (count > 0 && wave_live) {
+            const int vb = (count - 1) & 3;
+            // (no maximum has moved since these weights were computed)
+#pragma unroll
+            for (int x = 0; x < kPv; ++x) mul_v(kSubs == 1 ? 1 : (kSubs - 1) & 1, x, read_v(vb, kSubs - 1, x));
         }
 
         // ---- results
