@@ -137,7 +137,8 @@ __device__ __forceinline__ float add_pair(uint32_t pair, float sum) {
 }
 __device__ __forceinline__ uint32_t rest_pair(float a, float b, uint32_t pair) {
     const f16x2_v h = __builtin_bit_cast(f16x2_v, pair);
-    return round_pair<kGradF16>(a - (float)h[0], b - (float)h[1]);  // both differences exact
+    // both differences are exact; as fused operations they take the fp16 numbers as they are
+    return round_pair<kGradF16>(fmaf((float)h[0], -1.0f, a), fmaf((float)h[1], -1.0f, b));
 }
 
 // Exponent k that brings a row of queries whose largest magnitude is amax to

@@ -120,13 +120,40 @@ __device__ __forceinline__ int scale_exponent(float top) {
     return min(max((BITS == 8 ? 15 : 11) - e, -126), 126);
 }
 
-// Tiles of row tile `rt` of a sequence; *base: the first tile's first token.
+// Tiles of row tile `rt` of a sequence; base: the first tile's first token.
 template <int ROWS, int TILE>
 __device__ __forceinline__ int chunk_tiles(const KvqAttnArgs &a, const KvqSeq &s, int rt, int &base) {
     const int rows = s.len * a.group;
     const int t0 = rt * ROWS / a.group, t1 = (min(rows, (rt + 1) * ROWS) - 1) / a.group;
     base = kvq_lo(a, s, t0) & ~(TILE - 1);
     return max(1, (max(kvq_hi(s, t1) - base, 0) + TILE - 1) / TILE);
+}
+
+// What an item of a sequence is allotted in the line of work, in 1/16 tiles: row tile rt
+// has first + rt * step of them, its tiles (about) and what every item costs besides
+// them, 8 us before its first tile, which is three tiles' time.  Only the shares of
+// the work depend on it; it need not be exact, but its sums have to be had at once.
+struct ChunkShare {
+    int64_t first, step;
+    int32_t row_tiles;
+    __device__ __forceinline__ int64_t of(int rt) const { return first + rt * step; }
+    __device__ __forceinline__ int64_t before(int rt) const { return rt * first + (int64_t)rt * (rt - 1) / 2 * step; }
+};
+constexpr int kSetupTiles = 3;
+template <int ROWS, int TILE>
+__device__ __forceinline__ ChunkShare chunk_share(const KvqAttnArgs &a, const KvqSeq &s) {
+    ChunkShare r{0, 0, 0};
+    const int64_t rows = (int64_t)s.len * a.group;
+    if (rows <= a.max_rows) return r;
+    r.row_tiles = (int)((rows + ROWS - 1) / ROWS);
+    const int tokens = (ROWS + a.group - 1) / a.group;  // of a row tile
+    int reach = max(s.kv - s.len, 0) + tokens;
+    if (a.window > 0 && (int64_t)a.window + tokens < reach)
+        reach = a.window + tokens + TILE;  // and no more for later row tiles
+    else if (a.window == 0)
+        r.step = max(1, 16 * tokens / TILE);
+    r.first = 16 * kSetupTiles + 16 * (int64_t)reach / TILE + 1;
+    return r;
 }
 
 // A lane's outputs come in groups of four dimensions: register i_of of tile u_of holds
@@ -173,7 +200,7 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void k_kvq_chunk(KvqAttnArgs a) {
     ChunkPartial<GT, D, NW> *parts =
         reinterpret_cast<ChunkPartial<GT, D, NW> *>(static_cast<char *>(a.workspace) + kChunkMaxGroups * sizeof(ChunkSplit));
 
-    // ---- tiles of every sequence, as running sums
+    // ---- allotments of the sequences, as running sums
     {
         constexpr int kPer = (kChunkSeqs + S::kThreads - 1) / S::kThreads;
         int64_t u[kPer], sum = 0;
@@ -182,14 +209,8 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void k_kvq_chunk(KvqAttnArgs a) {
             const int b = tid * kPer + k;
             u[k] = 0;
             if (b < a.batch) {
-                const KvqSeq s = kvq_seq(a, b);
-                const int64_t rows = (int64_t)s.len * a.group;
-                if (rows > a.max_rows)
-                    for (int rt = 0; rt * (int64_t)S::kRows < rows; ++rt) {
-                        int base;
-                        u[k] += chunk_tiles<S::kRows, kTile>(a, s, rt, base);
-                    }
-                u[k] *= a.c.heads;
+                const ChunkShare r = chunk_share<S::kRows, kTile>(a, kvq_seq(a, b));
+                u[k] = r.before(r.row_tiles) * a.c.heads;
             }
             sum += u[k];
         }
@@ -212,7 +233,8 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void k_kvq_chunk(KvqAttnArgs a) {
         __syncthreads();
     }
     const int64_t total = uniform(s_pre[kChunkSeqs]);
-    const int64_t groups = min((int64_t)gridDim.x, total);
+    // (a stretch of less than four tiles is not worth its workgroup)
+    const int64_t groups = min((int64_t)gridDim.x, udiv(total + 63, 64));
     if (tid == 0) splits[blockIdx.x].last = -1;
     if ((int64_t)blockIdx.x >= groups) return;
     const int64_t each = udiv(total, groups), more = total - each * groups;
@@ -236,21 +258,31 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void k_kvq_chunk(KvqAttnArgs a) {
         seq.q0 = uniform(seq.q0);
         seq.len = uniform(seq.len);
         seq.kv = uniform(seq.kv);
+        const ChunkShare share = chunk_share<S::kRows, kTile>(a, seq);
         int64_t off = pos - uniform(s_pre[b]);
-        int rt = 0, base, tiles;
-        for (;; ++rt) {
-            tiles = chunk_tiles<S::kRows, kTile>(a, seq, rt, base);
-            if (off < (int64_t)tiles * a.c.heads) break;
-            off -= (int64_t)tiles * a.c.heads;
+        int rt = 0;
+        {
+            int hi = share.row_tiles;  // before(rt) * heads <= off < before(hi) * heads
+            while (hi - rt > 1) {
+                const int mid = (rt + hi) >> 1;
+                if (share.before(mid) * a.c.heads <= off) rt = mid; else hi = mid;
+            }
+            off -= share.before(rt) * a.c.heads;
         }
-        const int g = uniform((int)off / tiles), u0 = uniform((int)off % tiles);
-        const int64_t item_begin = pos - u0, item_end = item_begin + tiles;
+        int base;
+        const int tiles = chunk_tiles<S::kRows, kTile>(a, seq, rt, base);
+        const int64_t allotted = share.of(rt);
+        const int g = uniform((int)udiv(off, allotted));
+        const int64_t item_begin = pos - (off - g * allotted), item_end = item_begin + allotted;
         const int64_t seg_end = min(end, item_end);
+        // the stretch's part of the item's tiles
+        const int u0 = uniform((int)udiv((pos - item_begin) * tiles, allotted));
+        const int u1 = uniform((int)udiv((seg_end - item_begin) * tiles, allotted));
         const int r0 = rt * S::kRows, r1 = min(seq.len * a.group, r0 + S::kRows);
         const int t0 = r0 / a.group, t1 = (r1 - 1) / a.group;
         const int some_lo = kvq_lo(a, seq, t0), some_hi = kvq_hi(seq, t1);  // attended to by some row of the tile
         // (an item that attends to nothing reads nothing: the cache may have no pages)
-        const int from = base + u0 * kTile, count = some_hi > base ? (int)(seg_end - pos) : 0;
+        const int from = base + u0 * kTile, count = some_hi > base ? u1 - u0 : 0;
         const bool alone = pos == item_begin && seg_end == item_end;
 
         // ---- this lane's query row
@@ -264,13 +296,15 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void k_kvq_chunk(KvqAttnArgs a) {
         const int all_lo = wave_live ? kvq_lo(a, seq, wt1) : 0, all_hi = wave_live ? kvq_hi(seq, wt0) : 0;
         f16x8_v qf[kSteps];
         float qs;
+        uint4 raw[kSteps];
         {
             const int h = live ? g * a.group + r % a.group : 0;
             const uint16_t *src = a.q + (int64_t)(seq.q0 + my_t) * a.q_token_stride + (int64_t)h * a.q_head_stride;
-            uint4 raw[kSteps];
 #pragma unroll
             for (int s = 0; s < kSteps; ++s)
                 raw[s] = live ? *reinterpret_cast<const uint4 *>(src + 16 * s + 8 * half) : make_uint4(0, 0, 0, 0);
+        }
+        const auto make_queries = [&]() {
             float amax = 0.0f;
 #pragma unroll
             for (int s = 0; s < kSteps; ++s) {
@@ -295,7 +329,7 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void k_kvq_chunk(KvqAttnArgs a) {
             }
             qs = ldexpf(a.scale2, kOperandShift - kq);
             if (a.cap2 > 0.0f) qs *= a.cap_scale;
-        }
+        };
 
         // ---- the tiles' way from the cache into LDS
         const int32_t *table = a.table + (int64_t)b * a.table_stride;
@@ -304,9 +338,9 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void k_kvq_chunk(KvqAttnArgs a) {
         // (they are behind the sequence's end too, and so masked); a page outside the cache gives
         // rows of page 0, to be left out.
         const int last_page = (a.max_tokens >> a.c.shift) - 1;
-        const uint32_t pages = (uint32_t)min(a.c.n_pages, (int64_t)1 << 31);
+        const uint32_t in_cache = (uint32_t)min(a.c.n_pages, (int64_t)1 << 31);
         const auto page_of = [&](int j) -> int { return table[min(j >> a.c.shift, last_page)]; };
-        const auto there_is = [&](int page) { return (uint32_t)page < pages; };
+        const auto there_is = [&](int page) { return (uint32_t)page < in_cache; };
         const auto row_of = [&](int page, int j) -> int64_t {
             return (int64_t)((((uint64_t)(uint32_t)(there_is(page) ? page : 0) * (uint32_t)a.c.heads + (uint32_t)g)
                               << a.c.shift) |
@@ -318,75 +352,79 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void k_kvq_chunk(KvqAttnArgs a) {
         const auto first_token = [&](int i) { return (wave + i * NW) * kWaveTokens; };
         const int k_token = lane / (D / 16), k_dim = 16 * (lane % (D / 16));
         const int v_token = 4 * (lane / (D / 4)), v_dim = 4 * (lane % (D / 4));
-        uint32_t kw[kItems][S::kCodeWords], vw[kItems][4];
-        float kks[kItems], kvs[kItems];  // both scales of the piece's key row
-        float4 vvs[kItems];
-        int page[kItems], page_here[kItems];
         // tokens of the tile that a lane watches the scales of (two rounds for 128 tokens)
         constexpr int kWatch = kTile > 64 ? 2 : 1;
-        float w_ks[kWatch], w_vs[kWatch];
-        int w_page[kWatch], w_page_here[kWatch];
-        bool w_ok[kWatch], w_there[kWatch];
+        struct Pages {
+            int piece[kItems], watch[kWatch];
+        };
+        struct Stage {
+            uint32_t kw[kItems][S::kCodeWords], vw[kItems][4];
+            float kks[kItems], kvs[kItems];  // both scales of the piece's key row
+            float4 vvs[kItems];
+            int page[kItems];
+            float w_ks[kWatch], w_vs[kWatch];
+            bool w_ok[kWatch], w_there[kWatch];
+        };
         uint64_t there_next[kWatch];  // tokens whose pages are in the cache
         const auto watch_token = [&](int i) { return (64 * i + lane) % kTile; };
-        const auto load_pages = [&](int j) {
+        const auto load_pages = [&](Pages &p, int j) {
 #pragma unroll
-            for (int i = 0; i < kItems; ++i) page[i] = page_of(j + first_token(i));
+            for (int i = 0; i < kItems; ++i) p.piece[i] = page_of(j + first_token(i));
 #pragma unroll
-            for (int i = 0; i < kWatch; ++i) w_page[i] = page_of(j + watch_token(i));
+            for (int i = 0; i < kWatch; ++i) p.watch[i] = page_of(j + watch_token(i));
         };
-        // the pages loaded last are the next tile's
-        const auto take_pages = [&]() {
-#pragma unroll
-            for (int i = 0; i < kItems; ++i) page_here[i] = uniform(page[i]);
-#pragma unroll
-            for (int i = 0; i < kWatch; ++i) w_page_here[i] = w_page[i];
-        };
-        const auto load_tile = [&](int j) {
+        const auto load_tile = [&](Stage &s, const Pages &p, int j) {
 #pragma unroll
             for (int i = 0; i < kItems; ++i) {
-                const int64_t row = row_of(page_here[i], j + first_token(i));
+                s.page[i] = uniform(p.piece[i]);
+                const int64_t row = row_of(s.page[i], j + first_token(i));
                 const uint8_t *kp = a.c.codes[0] + row * kRowBytes, *vp = a.c.codes[1] + row * kRowBytes;
                 const float *ksp = a.c.scales[0] + row, *vsp = a.c.scales[1] + row;
-                kks[i] = ksp[k_token];
-                kvs[i] = vsp[k_token];
-                vvs[i] = *reinterpret_cast<const float4 *>(vsp + v_token);
+                s.kks[i] = ksp[k_token];
+                s.kvs[i] = vsp[k_token];
+                s.vvs[i] = *reinterpret_cast<const float4 *>(vsp + v_token);
                 kp += k_token * kRowBytes + k_dim * BITS / 8;
                 if (BITS == 8) {
                     const uint4 v = *reinterpret_cast<const uint4 *>(kp);
-                    kw[i][0] = v.x; kw[i][1] = v.y; kw[i][2 % S::kCodeWords] = v.z; kw[i][3 % S::kCodeWords] = v.w;
+                    s.kw[i][0] = v.x; s.kw[i][1] = v.y; s.kw[i][2 % S::kCodeWords] = v.z; s.kw[i][3 % S::kCodeWords] = v.w;
                 } else {
                     const uint2 v = *reinterpret_cast<const uint2 *>(kp);
-                    kw[i][0] = v.x; kw[i][1] = v.y;
+                    s.kw[i][0] = v.x; s.kw[i][1] = v.y;
                 }
                 vp += v_token * kRowBytes + v_dim * BITS / 8;
 #pragma unroll
                 for (int t = 0; t < 4; ++t)
-                    vw[i][t] = BITS == 8 ? *reinterpret_cast<const uint32_t *>(vp + t * kRowBytes)
-                                         : *reinterpret_cast<const uint16_t *>(vp + t * kRowBytes);
+                    s.vw[i][t] = BITS == 8 ? *reinterpret_cast<const uint32_t *>(vp + t * kRowBytes)
+                                           : *reinterpret_cast<const uint16_t *>(vp + t * kRowBytes);
             }
 #pragma unroll
             for (int i = 0; i < kWatch; ++i) {
                 const int at = j + watch_token(i);
-                const int64_t wr = row_of(w_page_here[i], at);
-                w_ks[i] = a.c.scales[0][wr];
-                w_vs[i] = a.c.scales[1][wr];
-                w_there[i] = there_is(w_page_here[i]);
-                w_ok[i] = w_there[i] & (at >= some_lo) & (at < some_hi);
+                const int64_t wr = row_of(p.watch[i], at);
+                s.w_ks[i] = a.c.scales[0][wr];
+                s.w_vs[i] = a.c.scales[1][wr];
+                s.w_there[i] = there_is(p.watch[i]);
+                s.w_ok[i] = s.w_there[i] & (at >= some_lo) & (at < some_hi);
             }
         };
+        Pages pages, pages0, pages1;
+        Stage stage;
+        if (count > 0) {
+            load_pages(pages0, from);
+            load_pages(pages1, from + kTile);
+        }
         // exponents of the scales: of the tile in LDS, and of the one being expanded
         float k_top = 0.0f, v_top = 0.0f;
         int k_exp_next = 126, v_exp_next = 126;
         float x_ks[kItems], x_kv[kItems], x_s4[kItems][4], kf, vf;
-        const auto expand_begin = [&](int j) {
+        const auto expand_begin = [&](const Stage &s, int j) {
             float kt = 0.0f, vt = 0.0f;
             bool plain = true;  // every token is attended to by some row and has finite scales
 #pragma unroll
             for (int i = 0; i < kWatch; ++i) {
-                const float x = fabsf(w_ks[i]), y = fabsf(w_vs[i]);
-                const bool in = w_ok[i] && x < INFINITY && y < INFINITY;
-                there_next[i] = __ballot(w_there[i]);
+                const float x = fabsf(s.w_ks[i]), y = fabsf(s.w_vs[i]);
+                const bool in = s.w_ok[i] && x < INFINITY && y < INFINITY;
+                there_next[i] = __ballot(s.w_there[i]);
                 plain = plain && __ballot(in) == ~0ull;
                 kt = fmaxf(kt, in ? x : 0.0f);
                 vt = fmaxf(vt, in ? y : 0.0f);
@@ -406,11 +444,11 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void k_kvq_chunk(KvqAttnArgs a) {
             vf = pow2(v_exp_next);
 #pragma unroll
             for (int i = 0; i < kItems; ++i) {
-                float ks = kks[i], kv = kvs[i], s4[4] = {vvs[i].x, vvs[i].y, vvs[i].z, vvs[i].w};
+                float ks = s.kks[i], kv = s.kvs[i], s4[4] = {s.vvs[i].x, s.vvs[i].y, s.vvs[i].z, s.vvs[i].w};
                 if (!plain) {
                     // a scale that is not finite makes the scores of its token NaN and its values 0: NaN
                     // for the rows that attend to it, nothing for the others
-                    const bool ok = there_is(page_here[i]);
+                    const bool ok = there_is(s.page[i]);
                     const int at = j + first_token(i) + k_token;
                     const bool in = ok && at >= some_lo && at < some_hi;
                     const bool finite = fabsf(ks) < INFINITY && fabsf(kv) < INFINITY;
@@ -430,12 +468,12 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void k_kvq_chunk(KvqAttnArgs a) {
         };
         // the expansion in pieces: the keys' row, then a dimension of the values at a time
         constexpr int kPieces = 5 * kItems;
-        const auto expand_piece = [&](int buf, int piece) {
+        const auto expand_piece = [&](const Stage &s, int buf, int piece) {
             const int i = piece / 5, d = piece % 5 - 1;
             if (d < 0) {
                 const f16x2_v scale = splat16(kExact ? kExactScale : x_ks[i] * kf);
                 uint4 x[2];
-                expand16<BITS>(kw[i], scale, scale * (_Float16)-0x1p-17f, x);
+                expand16<BITS>(s.kw[i], scale, scale * (_Float16)-0x1p-17f, x);
                 uint4 *dst = reinterpret_cast<uint4 *>(&s_k[buf][first_token(i) + k_token][k_dim]);
                 dst[0] = x[0];
                 dst[1] = x[1];
@@ -451,8 +489,8 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void k_kvq_chunk(KvqAttnArgs a) {
                 // multiplies lie together
                 const int quad = (first_token(i) + v_token) / 4;
                 const int to = 16 * (quad / 4) + 8 * (quad & 1) + 4 * ((quad >> 1) & 1);
-                const uint32_t lo = fma16(code_pair<BITS>(vw[i][0], vw[i][1], d), s2[0], s2[0] * (_Float16)-0x1p-17f);
-                const uint32_t hi = fma16(code_pair<BITS>(vw[i][2], vw[i][3], d), s2[1], s2[1] * (_Float16)-0x1p-17f);
+                const uint32_t lo = fma16(code_pair<BITS>(s.vw[i][0], s.vw[i][1], d), s2[0], s2[0] * (_Float16)-0x1p-17f);
+                const uint32_t hi = fma16(code_pair<BITS>(s.vw[i][2], s.vw[i][3], d), s2[1], s2[1] * (_Float16)-0x1p-17f);
                 *reinterpret_cast<uint2 *>(&s_v[buf][d * (D / 4) + v_dim / 4][to]) = make_uint2(lo, hi);
             }
         };
@@ -538,23 +576,25 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void k_kvq_chunk(KvqAttnArgs a) {
         if (count > 0) {
             // two tiles in LDS and the third on its way.  (Loads past the last tile are of rows that
             // exist; what is made of them is not used.)
-            load_pages(from);
-            take_pages();
-            load_pages(from + kTile);
-            load_tile(from);
+            Stage second;
+            load_tile(stage, pages0, from);
+            load_tile(second, pages1, from + kTile);
+            load_pages(pages, from + 2 * kTile);
+            make_queries();
             __syncthreads();  // the item before is done with the buffers
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
-                expand_begin(from + t * kTile);
+                expand_begin(t ? second : stage, from + t * kTile);
 #pragma unroll
-                for (int x = 0; x < kPieces; ++x) expand_piece(t, x);
+                for (int x = 0; x < kPieces; ++x) expand_piece(t ? second : stage, t, x);
                 k_exps[t] = k_exp_next;
                 v_exps[t] = v_exp_next;
 #pragma unroll
                 for (int i = 0; i < kWatch; ++i) theres[t][i] = there_next[i];
-                take_pages();
-                load_pages(from + (t + 2) * kTile);
-                load_tile(from + (t + 1) * kTile);
+                if (t == 0) {
+                    load_tile(stage, pages, from + 2 * kTile);
+                    load_pages(pages, from + 3 * kTile);
+                }
             }
             v_exp = v_exps[0];
             __syncthreads();
@@ -572,6 +612,11 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void k_kvq_chunk(KvqAttnArgs a) {
                 settle(acc[0], top, 0, 0, from, k_exps[0], theres[0]);
             }
         }
+        const auto load_next = [&](int j) {
+            const Pages p = pages;
+            load_pages(pages, j + 4 * kTile);
+            load_tile(stage, p, j + 3 * kTile);
+        };
         // A step is 32 tokens.  While its weights are computed, the matrix cores multiply the next
         // step's scores and the last step's values; in a tile's first step the tile after next is
         // expanded, too.  Four tiles' places in LDS: the one before this, whose last values are
@@ -580,12 +625,10 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void k_kvq_chunk(KvqAttnArgs a) {
             const int j = from + it * kTile, buf = it & 3, after = (it + 1) & 3, fresh = (it + 2) & 3;
             if (it > 0) __syncthreads();
             if (!wave_live) {
-                expand_begin(j + 2 * kTile);
+                expand_begin(stage, j + 2 * kTile);
 #pragma unroll
-                for (int x = 0; x < kPieces; ++x) expand_piece(fresh, x);
-                take_pages();
-                load_pages(j + 4 * kTile);
-                load_tile(j + 3 * kTile);
+                for (int x = 0; x < kPieces; ++x) expand_piece(stage, fresh, x);
+                load_next(j);
                 continue;
             }
 #pragma unroll
@@ -600,7 +643,7 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void k_kvq_chunk(KvqAttnArgs a) {
                 f16x8_v ahead[kAhead];
                 read_first<kN>(ahead, read);
                 if (sub == 0) {
-                    expand_begin(j + 2 * kTile);
+                    expand_begin(stage, j + 2 * kTile);
                     k_exps[2] = k_exp_next;
                     v_exps[2] = v_exp_next;
                 }
@@ -638,12 +681,10 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void k_kvq_chunk(KvqAttnArgs a) {
                 const auto piece = [&](int p) {
                     if (sub > 0) p += kFirst;
                     if (p < kPieces)
-                        expand_piece(fresh, p);
-                    else if (p < kFirst) {
-                        take_pages();
-                        load_pages(j + 4 * kTile);
-                        load_tile(j + 3 * kTile);
-                    } else if (p < kFirst + 8)
+                        expand_piece(stage, fresh, p);
+                    else if (p < kFirst)
+                        load_next(j);
+                    else if (p < kFirst + 8)
                         weigh(p - kFirst);
                     else
                         largest(4 * (p - kFirst - 8));
