@@ -47,11 +47,14 @@ struct ChunkShape {
     static constexpr bool kExact = GT == kGradF16;
     static constexpr int kThreads = 64 * NW, kRows = 32 * NW;
     static constexpr int kTile = D == 256 ? 32 : D == 128 ? 64 : 128;  // tokens
-    static constexpr int kItems = kTile * D / 16 / kThreads;           // rows' pieces a thread expands
+    // A thread expands 16 kWide key dimensions of a token and 4 kWide value dimensions of four.
+    static constexpr int kWide = kTile * D / 16 / kThreads;
+    static constexpr int kGroup = 4 * kWide;  // value dimensions of a thread
     static constexpr int kKeyRow = D + 8;                              // fp16 elements; 16 bytes of padding
     static constexpr int kValRow = kTile + 8;                          // spread the rows over the banks
     static constexpr int kCodeWords = BITS / 2;                        // words of 16 codes
-    static_assert(kItems >= 1 && kItems * kThreads == kTile * D / 16, "every thread expands whole pieces");
+    static constexpr int kValWords = BITS == 8 ? kWide : 1;            // words of a thread's codes of a value row
+    static_assert(kWide * kThreads == kTile * D / 16 && (kWide == 1 || kWide == 2), "every thread expands whole pieces");
 };
 
 // N products whose left operands come from LDS, kAhead reads in front, with the pieces
@@ -161,12 +164,10 @@ __device__ __forceinline__ ChunkShare chunk_share(const KvqAttnArgs &a, const Kv
 template <int D>
 struct ChunkOut {
     static constexpr int kQuads = D / 8;
-    static __device__ __forceinline__ constexpr int u_of(int q, int k) {
-        return D == 64 ? k >> 1 : D == 128 ? k : 2 * k + (q >> 4);
-    }
+    static __device__ __forceinline__ constexpr int u_of(int q, int k) { return D == 64 ? k >> 1 : 4 * (q >> 4) + k; }
     static __device__ __forceinline__ constexpr int i_of(int q, int k) { return D == 64 ? q + 8 * (k & 1) : q & 15; }
     static __device__ __forceinline__ int dim_of(int q, int half) {
-        return 4 * (32 * (q >> 4) + 8 * ((q & 15) >> 2) + 4 * half + (q & 3));
+        return (D == 256 ? 8 : 4) * (8 * ((q & 15) >> 2) + 4 * half + (q & 3)) + 4 * (q >> 4);
     }
 };
 
@@ -185,7 +186,7 @@ template <int GT, int D, int BITS, int NW>
 __global__ __launch_bounds__(64 * NW, NW / 4) void k_kvq_chunk(KvqAttnArgs a) {
     using S = ChunkShape<GT, D, BITS, NW>;
     constexpr bool kExact = S::kExact;
-    constexpr int kTile = S::kTile, kItems = S::kItems, kMTiles = D / 32, kSteps = D / 16;
+    constexpr int kTile = S::kTile, kWide = S::kWide, kMTiles = D / 32, kSteps = D / 16;
     constexpr int kOperandShift = kExact ? 9 : kCodeShift<BITS>;  // an operand is 2^-that of what it stands for
     constexpr float kExactScale = BITS == 8 ? kExactScale8 : kExactScale4;
     __shared__ _Float16 s_k[4][kTile][S::kKeyRow];
@@ -346,56 +347,65 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void k_kvq_chunk(KvqAttnArgs a) {
                               << a.c.shift) |
                              (uint32_t)(j & (a.c.page - 1)));
         };
-        // Piece i of a thread: 16 key dimensions of one token, and four value dimensions of four
-        // tokens.  A wave's pieces are of kWaveTokens consecutive tokens, in one page.
-        constexpr int kWaveTokens = 1024 / D, kRowBytes = D * BITS / 8;
-        const auto first_token = [&](int i) { return (wave + i * NW) * kWaveTokens; };
-        const int k_token = lane / (D / 16), k_dim = 16 * (lane % (D / 16));
-        const int v_token = 4 * (lane / (D / 4)), v_dim = 4 * (lane % (D / 4));
+        // A wave's threads expand consecutive tokens of one page, the same for keys and values.
+        constexpr int kRowBytes = D * BITS / 8, kGroup = S::kGroup;
+        const int first_token = wave * (1024 * kWide / D);
+        const int k_token = lane / (D / 16 / kWide), k_dim = 16 * kWide * (lane % (D / 16 / kWide));
+        const int v_token = 4 * (lane / (D / kGroup)), v_dim = kGroup * (lane % (D / kGroup));
         // tokens of the tile that a lane watches the scales of (two rounds for 128 tokens)
         constexpr int kWatch = kTile > 64 ? 2 : 1;
         struct Pages {
-            int piece[kItems], watch[kWatch];
+            int piece, watch[kWatch];
         };
         struct Stage {
-            uint32_t kw[kItems][S::kCodeWords], vw[kItems][4];
-            float kks[kItems], kvs[kItems];  // both scales of the piece's key row
-            float4 vvs[kItems];
-            int page[kItems];
+            uint32_t kw[kWide][S::kCodeWords], vw[4][S::kValWords];
+            float ks, kv;  // both scales of the key row
+            float4 vs;
+            int page;
             float w_ks[kWatch], w_vs[kWatch];
             bool w_ok[kWatch], w_there[kWatch];
         };
         uint64_t there_next[kWatch];  // tokens whose pages are in the cache
         const auto watch_token = [&](int i) { return (64 * i + lane) % kTile; };
         const auto load_pages = [&](Pages &p, int j) {
-#pragma unroll
-            for (int i = 0; i < kItems; ++i) p.piece[i] = page_of(j + first_token(i));
+            p.piece = page_of(j + first_token);
 #pragma unroll
             for (int i = 0; i < kWatch; ++i) p.watch[i] = page_of(j + watch_token(i));
         };
         const auto load_tile = [&](Stage &s, const Pages &p, int j) {
+            s.page = uniform(p.piece);
+            const int64_t row = row_of(s.page, j + first_token);
+            const float *ksp = a.c.scales[0] + row, *vsp = a.c.scales[1] + row;
+            s.ks = ksp[k_token];
+            s.kv = vsp[k_token];
+            s.vs = *reinterpret_cast<const float4 *>(vsp + v_token);
+            const uint32_t *kp = reinterpret_cast<const uint32_t *>(a.c.codes[0] + row * kRowBytes + k_token * kRowBytes +
+                                                                    k_dim * BITS / 8);
+            // (words of codes, as many at a time as a load takes)
+            constexpr int kKeyWords = kWide * S::kCodeWords;
+            uint32_t *kw = &s.kw[0][0];
+            if (kKeyWords == 2) {
+                const uint2 v = *reinterpret_cast<const uint2 *>(kp);
+                kw[0] = v.x; kw[1] = v.y;
+            } else {
 #pragma unroll
-            for (int i = 0; i < kItems; ++i) {
-                s.page[i] = uniform(p.piece[i]);
-                const int64_t row = row_of(s.page[i], j + first_token(i));
-                const uint8_t *kp = a.c.codes[0] + row * kRowBytes, *vp = a.c.codes[1] + row * kRowBytes;
-                const float *ksp = a.c.scales[0] + row, *vsp = a.c.scales[1] + row;
-                s.kks[i] = ksp[k_token];
-                s.kvs[i] = vsp[k_token];
-                s.vvs[i] = *reinterpret_cast<const float4 *>(vsp + v_token);
-                kp += k_token * kRowBytes + k_dim * BITS / 8;
-                if (BITS == 8) {
-                    const uint4 v = *reinterpret_cast<const uint4 *>(kp);
-                    s.kw[i][0] = v.x; s.kw[i][1] = v.y; s.kw[i][2 % S::kCodeWords] = v.z; s.kw[i][3 % S::kCodeWords] = v.w;
-                } else {
-                    const uint2 v = *reinterpret_cast<const uint2 *>(kp);
-                    s.kw[i][0] = v.x; s.kw[i][1] = v.y;
+                for (int t = 0; t < kKeyWords; t += 4) {
+                    const uint4 v = *reinterpret_cast<const uint4 *>(kp + t);
+                    kw[t] = v.x; kw[t + 1] = v.y; kw[t + 2] = v.z; kw[t + 3] = v.w;
                 }
-                vp += v_token * kRowBytes + v_dim * BITS / 8;
+            }
+            const uint8_t *vp = a.c.codes[1] + row * kRowBytes + v_token * kRowBytes + v_dim * BITS / 8;
 #pragma unroll
-                for (int t = 0; t < 4; ++t)
-                    s.vw[i][t] = BITS == 8 ? *reinterpret_cast<const uint32_t *>(vp + t * kRowBytes)
-                                           : *reinterpret_cast<const uint16_t *>(vp + t * kRowBytes);
+            for (int t = 0; t < 4; ++t) {
+                const uint8_t *q = vp + t * kRowBytes;
+                if (S::kValWords == 2) {
+                    const uint2 v = *reinterpret_cast<const uint2 *>(q);
+                    s.vw[t][0] = v.x;
+                    s.vw[t][S::kValWords - 1] = v.y;
+                } else {
+                    s.vw[t][0] = kGroup * BITS / 8 == 4 ? *reinterpret_cast<const uint32_t *>(q)
+                                                        : *reinterpret_cast<const uint16_t *>(q);
+                }
             }
 #pragma unroll
             for (int i = 0; i < kWatch; ++i) {
@@ -416,7 +426,7 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void k_kvq_chunk(KvqAttnArgs a) {
         // exponents of the scales: of the tile in LDS, and of the one being expanded
         float k_top = 0.0f, v_top = 0.0f;
         int k_exp_next = 126, v_exp_next = 126;
-        float x_ks[kItems], x_kv[kItems], x_s4[kItems][4], kf, vf;
+        float x_ks, x_kv, x_s4[4], kf, vf;  // scales of the tile being expanded, and their powers of two
         const auto expand_begin = [&](const Stage &s, int j) {
             float kt = 0.0f, vt = 0.0f;
             bool plain = true;  // every token is attended to by some row and has finite scales
@@ -442,56 +452,51 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void k_kvq_chunk(KvqAttnArgs a) {
             }
             kf = pow2(k_exp_next);
             vf = pow2(v_exp_next);
+            x_ks = s.ks;
+            x_kv = s.kv;
+            x_s4[0] = s.vs.x; x_s4[1] = s.vs.y; x_s4[2] = s.vs.z; x_s4[3] = s.vs.w;
+            if (!plain) {
+                // a scale that is not finite makes the scores of its token NaN and its values 0: NaN
+                // for the rows that attend to it, nothing for the others
+                const bool ok = there_is(s.page);
+                const int at = j + first_token + k_token;
+                const bool in = ok && at >= some_lo && at < some_hi;
+                const bool finite = fabsf(x_ks) < INFINITY && fabsf(x_kv) < INFINITY;
+                x_ks = in ? (finite ? x_ks : NAN) : 0.0f;
+                x_kv = in && finite ? x_kv : 0.0f;
 #pragma unroll
-            for (int i = 0; i < kItems; ++i) {
-                float ks = s.kks[i], kv = s.kvs[i], s4[4] = {s.vvs[i].x, s.vvs[i].y, s.vvs[i].z, s.vvs[i].w};
-                if (!plain) {
-                    // a scale that is not finite makes the scores of its token NaN and its values 0: NaN
-                    // for the rows that attend to it, nothing for the others
-                    const bool ok = there_is(s.page[i]);
-                    const int at = j + first_token(i) + k_token;
-                    const bool in = ok && at >= some_lo && at < some_hi;
-                    const bool finite = fabsf(ks) < INFINITY && fabsf(kv) < INFINITY;
-                    ks = in ? (finite ? ks : NAN) : 0.0f;
-                    kv = in && finite ? kv : 0.0f;
-#pragma unroll
-                    for (int t = 0; t < 4; ++t) {
-                        const int vat = j + first_token(i) + v_token + t;
-                        s4[t] = ok && vat >= some_lo && vat < some_hi && fabsf(s4[t]) < INFINITY ? s4[t] : 0.0f;
-                    }
+                for (int t = 0; t < 4; ++t) {
+                    const int vat = j + first_token + v_token + t;
+                    x_s4[t] = ok && vat >= some_lo && vat < some_hi && fabsf(x_s4[t]) < INFINITY ? x_s4[t] : 0.0f;
                 }
-                x_ks[i] = ks;
-                x_kv[i] = kv;
-#pragma unroll
-                for (int t = 0; t < 4; ++t) x_s4[i][t] = s4[t];
             }
         };
-        // the expansion in pieces: the keys' row, then a dimension of the values at a time
-        constexpr int kPieces = 5 * kItems;
+        // the expansion in pieces: 16 key dimensions, then a dimension of the values at a time
+        constexpr int kPieces = 5 * kWide;
         const auto expand_piece = [&](const Stage &s, int buf, int piece) {
-            const int i = piece / 5, d = piece % 5 - 1;
-            if (d < 0) {
-                const f16x2_v scale = splat16(kExact ? kExactScale : x_ks[i] * kf);
+            if (piece < kWide) {
+                const f16x2_v scale = splat16(kExact ? kExactScale : x_ks * kf);
                 uint4 x[2];
-                expand16<BITS>(s.kw[i], scale, scale * (_Float16)-0x1p-17f, x);
-                uint4 *dst = reinterpret_cast<uint4 *>(&s_k[buf][first_token(i) + k_token][k_dim]);
+                expand16<BITS>(s.kw[piece], scale, scale * (_Float16)-0x1p-17f, x);
+                uint4 *dst = reinterpret_cast<uint4 *>(&s_k[buf][first_token + k_token][k_dim + 16 * piece]);
                 dst[0] = x[0];
                 dst[1] = x[1];
-                if (kExact && k_dim == 0) {
-                    s_ks[buf][first_token(i) + k_token] = x_ks[i];
-                    s_vs[buf][first_token(i) + k_token] = x_kv[i] * vf;
+                if (kExact && k_dim == 0 && piece == 0) {
+                    s_ks[buf][first_token + k_token] = x_ks;
+                    s_vs[buf][first_token + k_token] = x_kv * vf;
                 }
             } else {
+                const int d = piece - kWide, w = BITS == 8 ? d / 4 : 0;
                 f16x2_v s2[2];
 #pragma unroll
-                for (int t = 0; t < 4; ++t) s2[t >> 1][t & 1] = (_Float16)(kExact ? kExactScale : x_s4[i][t] * vf);
+                for (int t = 0; t < 4; ++t) s2[t >> 1][t & 1] = (_Float16)(kExact ? kExactScale : x_s4[t] * vf);
                 // four tokens are eight bytes; of each 16 tokens, those that one half of a wave
                 // multiplies lie together
-                const int quad = (first_token(i) + v_token) / 4;
+                const int quad = (first_token + v_token) / 4;
                 const int to = 16 * (quad / 4) + 8 * (quad & 1) + 4 * ((quad >> 1) & 1);
-                const uint32_t lo = fma16(code_pair<BITS>(s.vw[i][0], s.vw[i][1], d), s2[0], s2[0] * (_Float16)-0x1p-17f);
-                const uint32_t hi = fma16(code_pair<BITS>(s.vw[i][2], s.vw[i][3], d), s2[1], s2[1] * (_Float16)-0x1p-17f);
-                *reinterpret_cast<uint2 *>(&s_v[buf][d * (D / 4) + v_dim / 4][to]) = make_uint2(lo, hi);
+                const uint32_t lo = fma16(code_pair<BITS>(s.vw[0][w], s.vw[1][w], d), s2[0], s2[0] * (_Float16)-0x1p-17f);
+                const uint32_t hi = fma16(code_pair<BITS>(s.vw[2][w], s.vw[3][w], d), s2[1], s2[1] * (_Float16)-0x1p-17f);
+                *reinterpret_cast<uint2 *>(&s_v[buf][d * (D / kGroup) + v_dim / kGroup][to]) = make_uint2(lo, hi);
             }
         };
 
@@ -816,9 +821,7 @@ __global__ __launch_bounds__(256) void k_kvq_chunk_join(KvqAttnArgs a) {
             for (int k = 0; k < 4; ++k) {
                 // the register's number, with `share` the only part that is not a constant
                 const int at = kMine * share + q;
-                const int u = D == 64 ? k >> 1 : D == 128 ? k : 2 * k + (at >> 4);
-                const int i = D == 64 ? at + 8 * (k & 1) : at & 15;
-                v[q][k] = fmaf(p.o[wave][16 * u + i][lane], f, v[q][k] * f0);
+                v[q][k] = fmaf(p.o[wave][16 * O::u_of(at, k) + O::i_of(at, k)][lane], f, v[q][k] * f0);
             }
     }
     const float inv = l != 0.0f ? 1.0f / l : 0.0f;
