@@ -4,17 +4,22 @@
 #include <math.h>
 
 #include <algorithm>
+#include <atomic>
 
 #include "kvq_chunk.h"
 #include "kvq_step.h"
 
 namespace onebit {
 
+// Compute units of the current device, asked for once for each device.
 static int compute_units() {
-    int dev = 0, cus = 256;
-    if (hipGetDevice(&dev) == hipSuccess) {
-        int v = 0;
-        if (hipDeviceGetAttribute(&v, hipDeviceAttributeMultiprocessorCount, dev) == hipSuccess && v > 0) cus = v;
+    static std::atomic<int> known[64];
+    int dev = 0;
+    if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= 64) return 256;
+    int cus = known[dev].load(std::memory_order_relaxed);
+    if (cus == 0) {
+        if (hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess || cus <= 0) return 256;
+        known[dev].store(cus, std::memory_order_relaxed);
     }
     return cus;
 }

@@ -437,15 +437,15 @@ class KvqCache(C.Structure):
                 ("page", _I), ("kv_heads", _I), ("head_dim", _I), ("bits", _I)]
 
 
-def _same_device(*tensors):
-    """The one device all the given tensors (None skipped) are on."""
-    devices = {t.device for t in tensors if t is not None}
-    for t in tensors:
-        if t is not None and not t.is_cuda:
-            raise TypeError(f"expected a device (GPU) tensor, got one on {t.device}")
-    if len(devices) != 1:
-        raise ValueError(f"all tensors of a call must be on one device, got {sorted(map(str, devices))}")
-    return devices.pop()
+def _same_device(first, *tensors) -> int:
+    """Index of the one device all the given tensors (None skipped) are on."""
+    index = first.get_device()                 # -1 for a host tensor
+    for t in (first, *tensors):
+        if t is not None and (t.get_device() != index or index < 0):
+            if not t.is_cuda:
+                raise TypeError(f"expected a device (GPU) tensor, got one on {t.device}")
+            raise ValueError(f"all tensors of a call must be on one device, got {first.device} and {t.device}")
+    return index
 
 
 def _dense(t, dtype, what):
@@ -462,24 +462,27 @@ def _kvq_cache(k_codes, k_scales, v_codes, v_scales, bits):
     import torch
     if bits not in (4, 8):
         raise ValueError(f"bits must be 4 or 8, got {bits}")
-    if k_codes.dim() != 4 or k_codes.shape != v_codes.shape:
+    shape = k_codes.shape
+    if len(shape) != 4 or shape != v_codes.shape:
         raise ValueError("k_codes and v_codes must both be [n_pages, kv_heads, page, head_dim * bits / 8]")
-    if k_scales.shape != k_codes.shape[:3] or v_scales.shape != k_codes.shape[:3]:
+    if k_scales.shape != shape[:3] or v_scales.shape != shape[:3]:
         raise ValueError("k_scales and v_scales must both be [n_pages, kv_heads, page]")
-    n_pages, heads, page, row = k_codes.shape
-    return KvqCache(_dense(k_codes, torch.uint8, "k_codes"), _dense(k_scales, torch.float32, "k_scales"),
-                    _dense(v_codes, torch.uint8, "v_codes"), _dense(v_scales, torch.float32, "v_scales"),
+    codes, scales = torch.uint8, torch.float32
+    n_pages, heads, page, row = shape
+    return KvqCache(_dense(k_codes, codes, "k_codes"), _dense(k_scales, scales, "k_scales"),
+                    _dense(v_codes, codes, "v_codes"), _dense(v_scales, scales, "v_scales"),
                     n_pages, page, heads, row * 8 // bits, bits)
 
 
 def _kvq_rows(t, heads, dim, what):
     """(token stride, head stride) of [tokens, heads, head_dim] rows whose innermost dimension is dense."""
-    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != dim:
-        raise ValueError(f"{what} must be [tokens, {heads}, {dim}], got {list(t.shape)}")
-    if t.stride(2) != 1:
+    shape, strides = t.shape, t.stride()
+    if len(shape) != 3 or shape[1] != heads or shape[2] != dim:
+        raise ValueError(f"{what} must be [tokens, {heads}, {dim}], got {list(shape)}")
+    if strides[2] != 1:
         raise ValueError(f"the innermost dimension of {what} must be contiguous")
     # the stride of a dimension of one entry is never used and may be anything
-    return (t.stride(0) if t.shape[0] > 1 else heads * dim), (t.stride(1) if heads > 1 else dim)
+    return (strides[0] if shape[0] > 1 else heads * dim), (strides[1] if heads > 1 else dim)
 
 
 def _kvq_slots(slots, tokens):
@@ -489,14 +492,24 @@ def _kvq_slots(slots, tokens):
     return _dense(slots, torch.int64, "slots")
 
 
-def _kvq_call(name, device, stream, *args):
+def _kvq_call(name, index, stream, *args):
     """Run the call with the tensors' device as the current one, on `stream` (default: that
     device's current stream)."""
     import torch
-    if stream is not None and not isinstance(stream, int) and stream.device != device:
-        raise ValueError(f"the stream is on {stream.device}, the tensors are on {device}")
-    with torch.cuda.device(device):
-        _check(getattr(load(), name)(*args, _stream(stream)), name)
+    if stream is None:
+        # the stream's number itself: building a Stream object takes longer than a small call's kernel
+        stream = torch._C._cuda_getCurrentRawStream(index)
+    elif not isinstance(stream, int):
+        if stream.device.index != index:
+            raise ValueError(f"the stream is on {stream.device}, the tensors are on cuda:{index}")
+        stream = stream.cuda_stream
+    call = getattr(_lib or load(), name)
+    if torch.cuda.current_device() == index:
+        status = call(*args, stream)
+    else:
+        with torch.cuda.device(index):
+            status = call(*args, stream)
+    _check(status, name)
 
 
 def kvq_quantize(k, v, slots, k_codes, k_scales, v_codes, v_scales, *, bits, stream=None):
