@@ -2,7 +2,10 @@
 // back.  A row (the head_dim values of one token and one cache head) becomes signed
 // levels of its own largest magnitude, to nearest:
 //   scale = amax / L,  code = z + rint(x * L / amax),  L = 2^(bits-1) - 1, z = 2^(bits-1).
-// Both are bound by HBM: a row is read once and written once.
+// Both are bound by HBM: a row is read once and written once.  Measured with nothing in
+// the caches, launch included (about 5 us): 16384 tokens of 8 heads of 128 from bf16 to
+// 4 bits 21.9 us (85 MB), back 20.1 us; 32768 tokens read back from 8 bits 39.1 us (204
+// MB).  A large copy runs at 4.8 TB/s.
 //
 // A lane holds eight consecutive values, so a row takes head_dim / 8 lanes of a wave
 // and its maximum a few lane exchanges.  A workgroup takes consecutive tokens of one
@@ -13,6 +16,7 @@
 namespace onebit {
 
 constexpr int kKvqBlock = 256;
+constexpr int kKvqRows = 4;  // of a thread
 
 // Rows whose largest magnitude is below this are stored as zeros: L / amax stays far
 // from overflow, and every scale that is not 0 is a normal number.
@@ -53,7 +57,8 @@ __device__ __forceinline__ void load8(const void *p, int64_t i, float (&f)[8]) {
         f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
         f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
     } else {
-        const uint4 h = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p) + i);
+        // (whole cache lines, read once: the streaming policy)
+        const uint4 h = ld_stream(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p) + i));
         const uint32_t w[4] = {h.x, h.y, h.z, h.w};
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
@@ -71,100 +76,133 @@ __device__ __forceinline__ uint32_t code_bits(float x, float inv) {
     return __float_as_uint(__fmaf_rn(x, inv, 12582912.0f + (float)KvqLevels<BITS>::kZero));
 }
 
+// The cache rows of a thread's rows, STEP apart; the head's first for those to be skipped.  All
+// slots are asked for at once and without a branch (the last one in place of those
+// behind it): the compiler would wait for each where the ways join.
+template <int STEP>
+__device__ __forceinline__ void cache_rows(const KvqCache &c, const int64_t *slots, int64_t first, int64_t tokens, int h,
+                                           int64_t (&row)[kKvqRows], bool (&ok)[kKvqRows]) {
+    int64_t slot[kKvqRows];
+#pragma unroll
+    for (int r = 0; r < kKvqRows; ++r) slot[r] = slots[min(first + r * STEP, tokens - 1)];
+#pragma unroll
+    for (int r = 0; r < kKvqRows; ++r) {
+        ok[r] = (first + r * STEP < tokens) & (slot[r] >= 0) & (slot[r] < c.n_slots);
+        const int64_t at = ok[r] ? slot[r] : 0;
+        row[r] = ((at >> c.shift) * c.heads + h) * c.page + (int32_t)(at & (c.page - 1));
+    }
+}
+
 template <int GT, int D, int BITS>
 __global__ __launch_bounds__(kKvqBlock) void k_kvq_quantize(KvqWriteArgs a) {
     constexpr int kLanes = D / 8, kRows = kKvqBlock / kLanes;
     const int sub = threadIdx.x % kLanes;
-    const int64_t i = (int64_t)blockIdx.x * kRows + threadIdx.x / kLanes;
     const int h = blockIdx.y >> 1, kv = blockIdx.y & 1;
-    // whole groups of kLanes lanes leave together, so the exchanges below see all of a row
-    if (i >= a.tokens) return;
-    const int64_t slot = a.slots[i];
-    if (slot < 0 || slot >= a.c.n_slots) return;
-    float f[8];
-    load8<GT>(a.src[kv], i * a.token_stride[kv] + h * a.head_stride[kv] + 8 * sub, f);
-    uint32_t top = 0;
+    const int64_t first = (int64_t)blockIdx.x * (kKvqRows * kRows) + threadIdx.x / kLanes;
+    int64_t row[kKvqRows];
+    bool ok[kKvqRows];
+    float f[kKvqRows][8];
+    cache_rows<kRows>(a.c, a.slots, first, a.tokens, h, row, ok);
 #pragma unroll
-    for (int k = 0; k < 8; ++k) top = max(top, __float_as_uint(f[k]) & 0x7fffffffu);
-    top = max_over_lanes<kLanes>(top);  // the order of magnitudes, infinity and NaN above all others
-    const float amax = __uint_as_float(top);
-    const bool finite = top < 0x7f800000u, live = finite && amax >= kKvqTiny;
-    const float L = (float)KvqLevels<BITS>::kTop;
-    const float inv = __fdiv_rn(L, live ? amax : L);
-    const float scale = live ? fminf(__fdiv_rn(amax, L), KvqLevels<BITS>::kMaxScale) : finite ? 0.0f : __uint_as_float(0x7fc00000u);
-    uint32_t c[8];
-#pragma unroll
-    for (int k = 0; k < 8; ++k) c[k] = code_bits<BITS>(f[k], inv);
-    const int64_t row =
-        ((slot >> a.c.shift) * a.c.heads + h) * a.c.page + (int32_t)(slot & (a.c.page - 1));
-    if (BITS == 8) {
-        uint32_t w[2];
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            const uint32_t lo = __builtin_amdgcn_perm(c[4 * k + 1], c[4 * k], 0x0c0c0400u);
-            const uint32_t hi = __builtin_amdgcn_perm(c[4 * k + 3], c[4 * k + 2], 0x0c0c0400u);
-            w[k] = live ? lo | (hi << 16) : 0x80808080u;
-        }
-        *reinterpret_cast<uint2 *>(a.c.codes[kv] + row * D + 8 * sub) = make_uint2(w[0], w[1]);
-    } else {
-        uint32_t w = 0;
-#pragma unroll
-        for (int k = 0; k < 8; ++k) w |= (c[k] & 15u) << (4 * k);
-        *reinterpret_cast<uint32_t *>(a.c.codes[kv] + row * (D / 2) + 4 * sub) = live ? w : 0x88888888u;
+    for (int r = 0; r < kKvqRows; ++r) {
+        // (a row that is skipped reads the call's first one)
+        const int64_t i = ok[r] ? first + r * kRows : 0;
+        load8<GT>(a.src[kv], i * a.token_stride[kv] + h * a.head_stride[kv] + 8 * sub, f[r]);
     }
-    if (sub == 0) a.c.scales[kv][row] = scale;
+#pragma unroll
+    for (int r = 0; r < kKvqRows; ++r) {
+        uint32_t top = 0;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) top = max(top, __float_as_uint(f[r][k]) & 0x7fffffffu);
+        top = max_over_lanes<kLanes>(top);  // the order of magnitudes, infinity and NaN above all others
+        if (!ok[r]) continue;
+        const float amax = __uint_as_float(top);
+        const bool finite = top < 0x7f800000u, live = finite && amax >= kKvqTiny;
+        const float L = (float)KvqLevels<BITS>::kTop;
+        const float inv = __fdiv_rn(L, live ? amax : L);
+        const float scale = live ? fminf(__fdiv_rn(amax, L), KvqLevels<BITS>::kMaxScale)
+                                 : finite ? 0.0f : __uint_as_float(0x7fc00000u);
+        uint32_t c[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) c[k] = code_bits<BITS>(f[r][k], inv);
+        if (BITS == 8) {
+            uint32_t w[2];
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const uint32_t lo = __builtin_amdgcn_perm(c[4 * k + 1], c[4 * k], 0x0c0c0400u);
+                const uint32_t hi = __builtin_amdgcn_perm(c[4 * k + 3], c[4 * k + 2], 0x0c0c0400u);
+                w[k] = live ? lo | (hi << 16) : 0x80808080u;
+            }
+            *reinterpret_cast<uint2 *>(a.c.codes[kv] + row[r] * D + 8 * sub) = make_uint2(w[0], w[1]);
+        } else {
+            uint32_t w = 0;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) w |= (c[k] & 15u) << (4 * k);
+            *reinterpret_cast<uint32_t *>(a.c.codes[kv] + row[r] * (D / 2) + 4 * sub) = live ? w : 0x88888888u;
+        }
+        if (sub == 0) a.c.scales[kv][row[r]] = scale;
+    }
 }
 
 template <int GT, int D, int BITS>
 __global__ __launch_bounds__(kKvqBlock) void k_kvq_dequantize(KvqReadArgs a) {
     constexpr int kLanes = D / 8, kRows = kKvqBlock / kLanes;
     const int sub = threadIdx.x % kLanes;
-    const int64_t i = (int64_t)blockIdx.x * kRows + threadIdx.x / kLanes;
     const int h = blockIdx.y >> 1, kv = blockIdx.y & 1;
-    if (i >= a.tokens) return;
-    const int64_t slot = a.slots[i];
-    if (slot < 0 || slot >= a.c.n_slots) return;
-    const int64_t row =
-        ((slot >> a.c.shift) * a.c.heads + h) * a.c.page + (int32_t)(slot & (a.c.page - 1));
-    const float scale = a.c.scales[kv][row];
-    float y[8];
-    if (BITS == 8) {
-        const uint2 w = *reinterpret_cast<const uint2 *>(a.c.codes[kv] + row * D + 8 * sub);
+    const int64_t first = (int64_t)blockIdx.x * (kKvqRows * kRows) + threadIdx.x / kLanes;
+    int64_t row[kKvqRows];
+    bool ok[kKvqRows];
+    uint32_t w[kKvqRows][2];
+    float scale[kKvqRows];
+    cache_rows<kRows>(a.c, a.slots, first, a.tokens, h, row, ok);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) y[k] = (float)(int)(((k < 4 ? w.x : w.y) >> (8 * (k & 3))) & 255u);
-    } else {
-        const uint32_t w = *reinterpret_cast<const uint32_t *>(a.c.codes[kv] + row * (D / 2) + 4 * sub);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) y[k] = (float)(int)((w >> (4 * k)) & 15u);
+    for (int r = 0; r < kKvqRows; ++r) {
+        scale[r] = a.c.scales[kv][row[r]];
+        if (BITS == 8) {
+            const uint2 v = *reinterpret_cast<const uint2 *>(a.c.codes[kv] + row[r] * D + 8 * sub);
+            w[r][0] = v.x;
+            w[r][1] = v.y;
+        } else {
+            w[r][0] = *reinterpret_cast<const uint32_t *>(a.c.codes[kv] + row[r] * (D / 2) + 4 * sub);
+        }
     }
 #pragma unroll
-    for (int k = 0; k < 8; ++k) y[k] = mul_rn(sub_rn(y[k], (float)KvqLevels<BITS>::kZero), scale);
-    const int64_t o = (i * a.c.heads + h) * D + 8 * sub;
-    if (GT == kGradF32) {
-        float4 *d = reinterpret_cast<float4 *>(static_cast<float *>(a.dst[kv]) + o);
-        d[0] = make_float4(y[0], y[1], y[2], y[3]);
-        d[1] = make_float4(y[4], y[5], y[6], y[7]);
-    } else {
-        *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.dst[kv]) + o) =
-            make_uint4(round_pair<GT>(y[0], y[1]), round_pair<GT>(y[2], y[3]), round_pair<GT>(y[4], y[5]),
-                       round_pair<GT>(y[6], y[7]));
+    for (int r = 0; r < kKvqRows; ++r) {
+        if (!ok[r]) continue;
+        float y[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const uint32_t c = BITS == 8 ? (w[r][k >> 2] >> (8 * (k & 3))) & 255u : (w[r][0] >> (4 * k)) & 15u;
+            y[k] = mul_rn(sub_rn((float)(int)c, (float)KvqLevels<BITS>::kZero), scale[r]);
+        }
+        const int64_t o = ((first + r * kRows) * a.c.heads + h) * D + 8 * sub;
+        if (GT == kGradF32) {
+            float4 *d = reinterpret_cast<float4 *>(static_cast<float *>(a.dst[kv]) + o);
+            d[0] = make_float4(y[0], y[1], y[2], y[3]);
+            d[1] = make_float4(y[4], y[5], y[6], y[7]);
+        } else {
+            *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.dst[kv]) + o) =
+                make_uint4(round_pair<GT>(y[0], y[1]), round_pair<GT>(y[2], y[3]), round_pair<GT>(y[4], y[5]),
+                           round_pair<GT>(y[6], y[7]));
+        }
     }
 }
 
+template <int D>
+static dim3 kvq_grid(int64_t tokens, int heads) {
+    constexpr int64_t each = (int64_t)kKvqRows * (kKvqBlock / (D / 8));
+    return dim3((unsigned)((tokens + each - 1) / each), 2 * heads);
+}
 template <int GT, int D, int BITS>
 static void launch_write(const KvqWriteArgs &a, hipStream_t s) {
-    constexpr int rows = kKvqBlock / (D / 8);
-    hipLaunchKernelGGL((k_kvq_quantize<GT, D, BITS>), dim3((unsigned)((a.tokens + rows - 1) / rows), 2 * a.c.heads),
-                       dim3(kKvqBlock), 0, s, a);
+    hipLaunchKernelGGL((k_kvq_quantize<GT, D, BITS>), kvq_grid<D>(a.tokens, a.c.heads), dim3(kKvqBlock), 0, s, a);
 }
 template <int GT, int D, int BITS>
 static void launch_read(const KvqReadArgs &a, hipStream_t s) {
-    constexpr int rows = kKvqBlock / (D / 8);
-    hipLaunchKernelGGL((k_kvq_dequantize<GT, D, BITS>), dim3((unsigned)((a.tokens + rows - 1) / rows), 2 * a.c.heads),
-                       dim3(kKvqBlock), 0, s, a);
+    hipLaunchKernelGGL((k_kvq_dequantize<GT, D, BITS>), kvq_grid<D>(a.tokens, a.c.heads), dim3(kKvqBlock), 0, s, a);
 }
 
-// f.template operator()<type, head_dim, bits>() for the runtime values
+// f.run<type, head_dim, bits>() for the runtime values
 template <int GT, int D, typename F>
 static void kvq_dispatch_bits(int bits, F f) {
     if (bits == 4)
@@ -204,7 +242,7 @@ struct ReadLaunch {
 };
 
 // Checks shared by both calls.  The grid has ceil(tokens / rows) x 2 heads workgroups
-// of at least 8 rows: fewer than 2^32 threads along x, at most 65535 workgroups along y.
+// of at least 32 rows: fewer than 2^32 threads along x, at most 65535 workgroups along y.
 static onebit_status_t kvq_check_rows(const kvq_cache_t *cache, onebit_dtype_t dtype, int64_t tokens, KvqCache *out) {
     if (dtype != ONEBIT_F32 && dtype != ONEBIT_BF16 && dtype != ONEBIT_F16) return ONEBIT_ERR_INVALID;
     if (tokens < 0 || tokens >= (1 << 26)) return ONEBIT_ERR_INVALID;
@@ -236,6 +274,7 @@ extern "C" onebit_status_t kvq_quantize(const void *k, const void *v, onebit_dty
     a.head_stride[1] = v_head_stride;
     a.slots = slots;
     a.tokens = tokens;
+    if (a.c.n_slots == 0) return ONEBIT_OK;  // every slot is outside the cache
     kvq_dispatch(dtype, cache->head_dim, cache->bits, WriteLaunch{a, static_cast<hipStream_t>(stream)});
     return hip_status(hipGetLastError());
 }
@@ -252,6 +291,7 @@ extern "C" onebit_status_t kvq_dequantize(const kvq_cache_t *cache, const int64_
     a.dst[1] = v_out;
     a.slots = slots;
     a.tokens = tokens;
+    if (a.c.n_slots == 0) return ONEBIT_OK;  // every slot is outside the cache
     kvq_dispatch(out_dtype, cache->head_dim, cache->bits, ReadLaunch{a, static_cast<hipStream_t>(stream)});
     return hip_status(hipGetLastError());
 }
