@@ -4,15 +4,15 @@
 //
 // Codes enter the matrix cores as they are.  A byte c in the low half of a 16-bit
 // word is, read as fp16, the subnormal number c * 2^-24: exact, and one byte
-// permutation makes two of them.  The matrix products therefore are of codes; what
-// the definition subtracts and scales stays outside of the sums:
-//   <q, k_j> = ks_j (<q, c_j> - z sum_d q_d),   out_d = sum_j w_j c_{j,d} - z sum_j w_j,
-// with w_j = p_j vs_j as the matrix cores see it (after its rounding), so the second
-// identity is exact and the rounding's error is relative to |v|, not to the codes'
-// offset.  A 4-bit code is put into the byte's high nibble.  (The matrix cores align
-// the products by the operands' exponent fields, where all subnormal numbers count as
-// 2^-14: a product is summed as exactly as if its code were 1024, eight times the
-// largest magnitude.  4-bit codes left in the low nibble would lose four bits more.)
+// permutation makes two of them.  Scores are sums over codes; what the definition
+// subtracts and scales stays outside of the sum:
+//   <q, k_j> = ks_j (<q, c_j> - z sum_d q_d).
+// (The matrix cores align the products by the operands' exponent fields, where all
+// subnormal numbers count as 2^-14: a product is summed as exactly as if its code were
+// 1024, eight times the largest magnitude.  A 4-bit code is put into the byte's high
+// nibble; in the low one it would lose four bits more.)  Values, whose sum is over
+// thousands of tokens and may come out far smaller than the codes' offset z, enter as
+// (c - z) 2^-9, exact too, one fused operation more for two of them.
 #pragma once
 
 #include "kvq_common.h"
@@ -132,14 +132,28 @@ __device__ __forceinline__ uint32_t code_pair(uint32_t wa, uint32_t wb, int u) {
 template <int GT>
 constexpr bool kTwoPart = GT == kGradF16;
 
-__device__ __forceinline__ float add_pair(uint32_t pair, float sum) {
-    return __builtin_amdgcn_fdot2(__builtin_bit_cast(f16x2_v, pair), (f16x2_v){(_Float16)1, (_Float16)1}, sum, false);
-}
 __device__ __forceinline__ uint32_t rest_pair(float a, float b, uint32_t pair) {
     const f16x2_v h = __builtin_bit_cast(f16x2_v, pair);
     // both differences are exact; as fused operations they take the fp16 numbers as they are
     return round_pair<kGradF16>(fmaf((float)h[0], -1.0f, a), fmaf((float)h[1], -1.0f, b));
 }
+
+__device__ __forceinline__ f16x2_v splat16(float v) {
+    const _Float16 h = (_Float16)v;
+    return (f16x2_v){h, h};
+}
+__device__ __forceinline__ uint32_t fma16(uint32_t codes, f16x2_v scale, f16x2_v offset) {
+    return __builtin_bit_cast(uint32_t, __builtin_elementwise_fma(__builtin_bit_cast(f16x2_v, codes), scale, offset));
+}
+
+// A code operand times kUnitScale, less kUnitOffset: (c - z) 2^-kUnitShift, exactly, in one
+// fused operation for two.
+template <int BITS>
+constexpr float kUnitScale = BITS == 8 ? 0x1p15f : 0x1p11f;
+// z as an operand is 2^-17 at either width
+template <int BITS>
+constexpr float kUnitOffset = kUnitScale<BITS> * 0x1p-17f;
+constexpr int kUnitShift = 9;
 
 // Exponent k that brings a row of queries whose largest magnitude is amax to
 // [2^14, 2^15) as fp16: exact for bf16 and fp16 values down to 2^-29 of the largest,

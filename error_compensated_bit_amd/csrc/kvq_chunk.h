@@ -93,14 +93,6 @@ __device__ __forceinline__ void weave(f16x8_v (&f)[kAhead], Read read, Product p
     }
 }
 
-__device__ __forceinline__ f16x2_v splat16(float v) {
-    const _Float16 h = (_Float16)v;
-    return (f16x2_v){h, h};
-}
-__device__ __forceinline__ uint32_t fma16(uint32_t codes, f16x2_v scale, f16x2_v offset) {
-    return __builtin_bit_cast(uint32_t, __builtin_elementwise_fma(__builtin_bit_cast(f16x2_v, codes), scale, offset));
-}
-
 // 16 consecutive codes to fp16, in the order of query_operand
 template <int BITS>
 __device__ __forceinline__ void expand16(const uint32_t (&w)[BITS / 2], f16x2_v scale, f16x2_v offset, uint4 (&out)[2]) {
@@ -112,9 +104,6 @@ __device__ __forceinline__ void expand16(const uint32_t (&w)[BITS / 2], f16x2_v 
                             fma16(c.w, scale, offset));
     }
 }
-
-// (c - z) 2^-9 from a code operand
-constexpr float kExactScale8 = 32768.0f, kExactScale4 = 2048.0f;
 
 // The exponent by which scales up to `top` are taken so that they use fp16's range
 template <int BITS>
@@ -187,8 +176,8 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void k_kvq_chunk(KvqAttnArgs a) {
     using S = ChunkShape<GT, D, BITS, NW>;
     constexpr bool kExact = S::kExact;
     constexpr int kTile = S::kTile, kWide = S::kWide, kMTiles = D / 32, kSteps = D / 16;
-    constexpr int kOperandShift = kExact ? 9 : kCodeShift<BITS>;  // an operand is 2^-that of what it stands for
-    constexpr float kExactScale = BITS == 8 ? kExactScale8 : kExactScale4;
+    constexpr int kOperandShift = kExact ? kUnitShift : kCodeShift<BITS>;  // an operand is 2^-that of what it stands for
+    constexpr float kExactScale = kUnitScale<BITS>;
     __shared__ _Float16 s_k[4][kTile][S::kKeyRow];
     __shared__ _Float16 s_v[4][D][S::kValRow];
     __shared__ float s_ks[4][kExact ? kTile : 1], s_vs[4][kExact ? kTile : 1];

@@ -260,11 +260,11 @@ __global__ __launch_bounds__(kStepBlock, NT == 1 && D <= 128 ? 3 : 2) void k_kvq
 
         // ---- the loop over this wave's tiles of 32 tokens
         f32x4_v o[NT][T::kDims];
-        float m[NT], l[NT], wsum[NT];
+        float m[NT], l[NT];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             m[nt] = kNone;
-            l[nt] = wsum[nt] = 0.0f;
+            l[nt] = 0.0f;
 #pragma unroll
             for (int u = 0; u < T::kDims; ++u) o[nt][u] = (f32x4_v){0.0f, 0.0f, 0.0f, 0.0f};
         }
@@ -364,7 +364,6 @@ __global__ __launch_bounds__(kStepBlock, NT == 1 && D <= 128 ? 3 : 2) void k_kvq
                     const float f = exp2_fast(m[nt] - top);
                     m[nt] = top;
                     l[nt] *= f;
-                    wsum[nt] *= f;
 #pragma unroll
                     for (int u = 0; u < T::kDims; ++u) o[nt][u] *= f;
                 }
@@ -389,7 +388,6 @@ __global__ __launch_bounds__(kStepBlock, NT == 1 && D <= 128 ? 3 : 2) void k_kvq
                 const int e = value_exponent(v_top);
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
-                    wsum[nt] = ldexpf(wsum[nt], e - kv_exp);
 #pragma unroll
                     for (int u = 0; u < T::kDims; ++u)
 #pragma unroll
@@ -420,11 +418,7 @@ __global__ __launch_bounds__(kStepBlock, NT == 1 && D <= 128 ? 3 : 2) void k_kvq
                         l[nt] += e[i];
                     }
                     pw[k >> 1] = round_pair<kGradF16>(p[0], p[1]);
-                    wsum[nt] = add_pair(pw[k >> 1], wsum[nt]);
-                    if (kTwoPart<GT>) {
-                        lw[k >> 1] = rest_pair(p[0], p[1], pw[k >> 1]);
-                        wsum[nt] = add_pair(lw[k >> 1], wsum[nt]);
-                    }
+                    if (kTwoPart<GT>) lw[k >> 1] = rest_pair(p[0], p[1], pw[k >> 1]);
                 }
                 pf[nt] = __builtin_bit_cast(f16x8_v, (u32x4_v){pw[0], pw[1], pw[2], pw[3]});
                 if (kTwoPart<GT>) pl[nt] = __builtin_bit_cast(f16x8_v, (u32x4_v){lw[0], lw[1], lw[2], lw[3]});
@@ -432,8 +426,11 @@ __global__ __launch_bounds__(kStepBlock, NT == 1 && D <= 128 ? 3 : 2) void k_kvq
 #pragma unroll
             for (int u = 0; u < T::kDims; ++u) {
                 const int w = u * BITS / 32;
-                const u32x4_v av = {code_pair<BITS>(vw[0][0][w], vw[0][1][w], u), code_pair<BITS>(vw[0][2][w], vw[0][3][w], u),
-                                    code_pair<BITS>(vw[1][0][w], vw[1][1][w], u), code_pair<BITS>(vw[1][2][w], vw[1][3][w], u)};
+                const f16x2_v unit = splat16(kUnitScale<BITS>), zero = splat16(-kUnitOffset<BITS>);
+                const u32x4_v av = {fma16(code_pair<BITS>(vw[0][0][w], vw[0][1][w], u), unit, zero),
+                                    fma16(code_pair<BITS>(vw[0][2][w], vw[0][3][w], u), unit, zero),
+                                    fma16(code_pair<BITS>(vw[1][0][w], vw[1][1][w], u), unit, zero),
+                                    fma16(code_pair<BITS>(vw[1][2][w], vw[1][3][w], u), unit, zero)};
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
                     o[nt][u] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8_v, av), pf[nt], o[nt][u], 0, 0, 0);
@@ -447,7 +444,6 @@ __global__ __launch_bounds__(kStepBlock, NT == 1 && D <= 128 ? 3 : 2) void k_kvq
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             l[nt] = over_quarters_sum(l[nt]);
-            wsum[nt] = over_quarters_sum(wsum[nt]);
             if (c == 0) {
                 s_m[wave][16 * nt + n] = m[nt];
                 s_l[wave][16 * nt + n] = l[nt];
@@ -471,7 +467,7 @@ __global__ __launch_bounds__(kStepBlock, NT == 1 && D <= 128 ? 3 : 2) void k_kvq
             for (int u = 0; u < T::kDims; ++u) {
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    o[nt][u][i] = ldexpf((o[nt][u][i] - kOffset * wsum[nt]) * f, kCodeShift<BITS> - kv_exp);
+                    o[nt][u][i] = ldexpf(o[nt][u][i] * f, kUnitShift - kv_exp);
                 }
                 *reinterpret_cast<f32x4_v *>(dst + 16 * u) = o[nt][u];
             }
