@@ -262,6 +262,17 @@ def test_rows_that_attend_to_nothing(q_len, bits):
     assert (got[:q_len] == 0).all() and (lse[:q_len] == -math.inf).all()
 
 
+@pytest.mark.parametrize("window", [2 ** 31 - 1, 2 ** 31 - 20, 2 ** 30])
+@pytest.mark.parametrize("q_len", [7, 48])
+def test_the_widest_windows(window, q_len):
+    """A window that reaches far in front of the first token, with queries that stand there."""
+    lens = torch.tensor([0, 4, 47, q_len, 200], dtype=torch.int32)
+    g = gen("widest", q_len)
+    q, pools, table, _, _ = make(g, [q_len] * 5, [0, 4, 47, q_len, 200], 8, 2, 64, 16, 8, BF16)
+    got, lse = attend(q, pools, table, lens, 8, window=window)
+    check(got, lse, kvq_ref.attention(q, pools, table, lens, bits=8, scale=0.125), BF16)
+
+
 @pytest.mark.parametrize("q_len", [1, 70])
 @pytest.mark.parametrize("bits", [4, 8])
 def test_unattended_positions_have_no_influence(q_len, bits):
