@@ -429,6 +429,7 @@ onebit_status_t qsdp_mean_abs_error(const uint16_t *x_bf16, const double *ysum, 
  * block_table[t / page] of the cache, at offset t % page.  A slot is a token's place
  * in the whole cache: page number * page + offset.
  *
+ * The calls below are not among the classes of the launch timing above.
  * bits 4 or 8; head_dim 64, 128 or 256 (ONEBIT_ERR_UNSUPPORTED otherwise); page
  * a power of two from 16 to 1024; kv_heads from 1 to 32767; n_pages >= 0 and
  * n_pages * page < 2^47.  Codes and scales are 16-byte aligned.  The struct is a host struct, read
@@ -475,10 +476,17 @@ onebit_status_t kvq_dequantize(const kvq_cache_t *cache, const int64_t *slots, i
  * all j <= p):
  *   s_j = sm_scale * sum_d q_d k_{j,d};   softcap > 0: s_j = softcap * tanh(s_j / softcap)
  *   out = sum_j exp(s_j - lse) v_j,       lse = log sum_j exp(s_j)
- * with k, v the values read back (scaled outside the sums, not rounded).  A query that
- * attends to nothing (p < 0) gets out = 0 and lse = -inf.  Sums, maxima and lse are
- * binary32; the weights exp(s_j - max) * v_scale_j enter the second sum as fp16 (11
- * bits, ties to even) relative to the row's largest.
+ * with k, v the values read back.  A query that attends to nothing (p < 0) gets out = 0
+ * and lse = -inf.  Sums, maxima and lse are binary32.  Roundings before them: of the
+ * weights exp(s_j - max) to fp16 (11 bits, ties to even) for bf16 outputs, to two fp16
+ * parts for fp16 ones; and, for bf16 and sequences with more than 32 query rows of a
+ * cache head (tokens * q_heads / kv_heads), of the keys and values to fp16 (their scale
+ * and their product with it, an eighth of an 8-bit code's own step or less).  Weights
+ * and values that far below the largest of their tiles fall out of fp16's range are
+ * lost (2^-31 of the largest weight, 2^-14 of the largest scale at most).  A scale that
+ * is not finite makes out and lse NaN, or out alone, for the queries that attend to its
+ * row, and nothing for the others.
+ * NULL q_offsets is the form for single tokens and drafts: one launch instead of three.
  * q: bf16 or fp16 (ONEBIT_ERR_UNSUPPORTED otherwise), addressed as k above.  out:
  * [total_q][q_heads][head_dim], contiguous, of q's type.  lse: fp32 [total_q][q_heads],
  * nullable.  Rows of q that belong to no sequence leave out and lse as they were.
