@@ -484,8 +484,8 @@ onebit_status_t kvq_dequantize(const kvq_cache_t *cache, const int64_t *slots, i
  * and their product with it, an eighth of an 8-bit code's own step or less).  Weights
  * and values that far below the largest of their tiles fall out of fp16's range are
  * lost (2^-31 of the largest weight, 2^-14 of the largest scale at most).  A scale that
- * is not finite makes out and lse NaN, or out alone, for the queries that attend to its
- * row, and nothing for the others.
+ * is not finite leaves nothing finite in out (nor, maybe, in lse) for the queries that
+ * attend to its row, and makes no difference to the others.
  * NULL q_offsets is the form for single tokens and drafts: one launch instead of three.
  * q: bf16 or fp16 (ONEBIT_ERR_UNSUPPORTED otherwise), addressed as k above.  out:
  * [total_q][q_heads][head_dim], contiguous, of q's type.  lse: fp32 [total_q][q_heads],

@@ -348,6 +348,24 @@ def test_a_nan_scale_that_is_attended_to_gives_nan(q_len, which):
         assert torch.isnan(lse[q_len:, 2:]).all()
 
 
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("q_len,kv,at", [(5, 90, 87), (70, 100, 83), (300, 300, 140)])
+@pytest.mark.parametrize("which,bad", [(1, math.nan), (3, math.nan), (3, math.inf)])
+def test_a_bad_scale_concerns_only_those_who_attend_to_it(dtype, q_len, kv, at, which, bad):
+    """A row whose scale is not finite, in the middle of the new tokens: nothing finite from it on (an
+    infinite value times a weight is one, by the formula), and as before it without it."""
+    g = gen("bad", q_len)
+    q, pools, table, lens, offs = make(g, [q_len], [kv], 4, 2, 64, 16, 8, dtype)
+    ref = kvq_ref.attention(q, pools, table, lens, bits=8, scale=0.125)
+    dirty = [p.clone() for p in pools]
+    dirty[which][int(table[0, at // 16]), :, at % 16] = bad
+    got, _ = attend(q, tuple(dirty), table, lens, 8)
+    first = at - (kv - q_len)                       # the query that stands at the row
+    assert torch.isnan(got[first:]).all() if math.isnan(bad) else not torch.isfinite(got[first:]).any()
+    cut = tuple(t[:first] for t in ref)
+    check(got[:first], None, cut, dtype)
+
+
 @pytest.mark.parametrize("q_len", [1, 70])
 @pytest.mark.parametrize("v_size", [1e-30, 1e-3, 1.0, 1e5, 1e30])
 def test_values_of_any_size(q_len, v_size):
@@ -465,6 +483,95 @@ def test_a_long_cache_split_along_its_length(bits, dim, hq, heads, q_len):
     for _ in range(3):
         again, l2 = attend(q, pools, table, lens, bits, q_offsets=offs)
         assert torch.equal(got, again) and torch.equal(lse, l2)
+
+
+@pytest.mark.parametrize("hq,heads,dim,dtype", [(1, 1, 64, F16), (8, 2, 128, BF16), (2, 1, 256, BF16)])
+def test_a_chunk_over_a_long_cache(hq, heads, dim, dtype):
+    """One chunk, few heads: each row tile is split over many workgroups and joined."""
+    g = gen("long chunk", dim)
+    q, pools, table, lens, offs = make(g, [70], [20011], hq, heads, dim, 64, 8, dtype)
+    got, lse = attend(q, pools, table, lens, 8, q_offsets=offs)
+    check(got, lse, kvq_ref.attention(q, pools, table, lens, bits=8, scale=dim ** -0.5, q_offsets=offs), dtype)
+    for _ in range(3):
+        again, l2 = attend(q, pools, table, lens, 8, q_offsets=offs)
+        assert torch.equal(got, again) and torch.equal(lse, l2)
+
+
+@pytest.mark.parametrize("hq,heads,dim", [(600, 2, 64), (257, 1, 128), (300, 1, 256)])
+def test_more_query_heads_of_a_cache_head_than_a_tile_has_rows(hq, heads, dim):
+    g = gen("group", hq)
+    q, pools, table, lens, offs = make(g, [1, 3, 0, 2], [33, 70, 5, 2], hq, heads, dim, 16, 8, BF16)
+    got, lse = attend(q, pools, table, lens, 8, q_offsets=offs)
+    check(got, lse, kvq_ref.attention(q, pools, table, lens, bits=8, scale=dim ** -0.5, q_offsets=offs), BF16)
+
+
+@pytest.mark.parametrize("n,q_len", [(1024, 1), (1025, 1), (2100, 2), (512, 40), (1300, 33)])
+def test_more_sequences_than_a_launch_takes(n, q_len):
+    g = gen("launches", n)
+    ks = torch.randint(q_len, q_len + 30, (n,), generator=g).tolist()
+    q, pools, table, lens, offs = make(g, [q_len] * n, ks, 1, 1, 64, 16, 8, BF16)
+    got, lse = attend(q, pools, table, lens, 8)
+    check(got, lse, kvq_ref.attention(q, pools, table, lens, bits=8, scale=0.125), BF16)
+    again, _ = attend(q, pools, table, lens, 8, q_offsets=offs)
+    assert torch.equal(got, again)
+
+
+def test_one_workspace_for_calls_of_every_size():
+    """A workspace is ready for the next call, whatever that one's sizes; two captured graphs that are
+    replayed one after the other may share it."""
+    g = gen("workspace")
+    calls = []
+    for qs, ks, hq, heads, dim, dtype in [([1] * 3, [3000, 200, 5000], 8, 2, 128, BF16), ([90], [4000], 2, 2, 64, F16),
+                                          ([1, 40, 7], [2500, 700, 7], 4, 2, 256, BF16), ([1], [6000], 1, 1, 64, F16),
+                                          ([3] * 5, [900, 20, 4000, 3, 1], 20, 1, 128, F16)]:
+        q, pools, table, lens, offs = make(g, qs, ks, hq, heads, dim, 16, 8, dtype)
+        want, _ = attend(q, pools, table, lens, 8, q_offsets=offs)
+        size = ob.kvq_attention_workspace_bytes(len(qs), q.shape[0], hq, heads, dim)
+        calls.append((dev((q, *pools, table, lens, offs)), want, size))
+    ws = torch.zeros(max(c[2] for c in calls), dtype=torch.uint8, device=DEV)
+
+    def run(c, out):
+        q, kc, ks, vc, vs, table, lens, offs = c[0]
+        ob.kvq_attention(q, kc, ks, vc, vs, table, lens, out, bits=8, q_offsets=offs, workspace=ws)
+
+    outs = [torch.zeros_like(c[0][0]) for c in calls]
+    for _ in range(3):
+        for c, out in zip(calls, outs):
+            out.zero_()
+            run(c, out)
+            assert torch.equal(out.cpu(), c[1])
+    graphs = []
+    for c, out in zip(calls, outs):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            run(c, out)
+        graphs.append(graph)
+    for i in (0, 1, 2, 3, 4, 2, 0, 0, 3, 1, 4):
+        outs[i].zero_()
+        graphs[i].replay()
+        torch.cuda.synchronize()
+        assert torch.equal(outs[i].cpu(), calls[i][1]), i
+
+
+def test_a_stream_given_by_number():
+    g = gen("number")
+    q, pools, table, lens, _ = make(g, [1] * 2, [300, 40], 4, 2, 64, 16, 8, BF16)
+    want, _ = attend(q, pools, table, lens, 8)
+    side = torch.cuda.Stream()
+    qd, pd, td, ld = q.to(DEV), dev(pools), table.to(DEV), lens.to(DEV)
+    out = torch.zeros_like(qd)
+    ws = torch.zeros(ob.kvq_attention_workspace_bytes(2, 2, 4, 2, 64), dtype=torch.uint8, device=DEV)
+    torch.cuda.synchronize()
+    ob.kvq_attention(qd, *pd, td, ld, out, bits=8, workspace=ws, stream=side.cuda_stream)
+    side.synchronize()
+    assert torch.equal(out.cpu(), want)
+    # the current stream is the one taken otherwise
+    out.zero_()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        ob.kvq_attention(qd, *pd, td, ld, out, bits=8, workspace=ws)
+    side.synchronize()
+    assert torch.equal(out.cpu(), want)
 
 
 @pytest.mark.parametrize("q_max", [1, 90])
