@@ -80,7 +80,8 @@ static void launch(KvqAttnArgs a, hipStream_t s) {
             KvqAttnArgs x = slice(a, b, kChunkSeqs);
             x.workspace = static_cast<char *>(a.workspace) + kStepHeader;
             hipLaunchKernelGGL((k_kvq_chunk<GT, D, BITS, kWaves>), dim3(chunk_groups()), dim3(64 * kWaves), 0, s, x);
-            hipLaunchKernelGGL((k_kvq_chunk_join<GT, D, kWaves>), dim3(chunk_groups(), kWaves), dim3(256), 0, s, x);
+            hipLaunchKernelGGL((k_kvq_chunk_join<GT, D, kWaves>), dim3(8 * compute_units()), dim3(64 * kJoinWaves), 0, s, x,
+                               chunk_groups());
         }
     }
 }

@@ -30,10 +30,12 @@ constexpr int kChunkMaxGroups = 1024;  // workgroups of one launch
 
 // What workgroup w leaves for the join of the item that it begins and does not end.
 struct ChunkSplit {
-    int32_t last;   // the item's last workgroup; -1: there is no such item
-    int32_t slot;   // of its first part
-    int32_t seq, tile, head;
-    int32_t pad[3];
+    int32_t last;  // the item's last workgroup; -1: there is no such item
+    int32_t slot;  // of its first part
+    int32_t q0;    // the sequence's first query
+    int32_t row, rows;  // the item's first query row of the sequence, and how many
+    int32_t head;
+    int32_t pad[2];
 };
 
 template <int GT, int D, int NW>
@@ -164,8 +166,8 @@ template <int GT>
 __device__ __forceinline__ void store_four(const KvqAttnArgs &a, int64_t row, int d, int dims, const float (&v)[4]) {
     *reinterpret_cast<uint2 *>(a.out + row * dims + d) = make_uint2(round_pair<GT>(v[0], v[1]), round_pair<GT>(v[2], v[3]));
 }
-__device__ __forceinline__ int64_t out_row(const KvqAttnArgs &a, const KvqSeq &s, int g, int r) {
-    return (int64_t)(s.q0 + r / a.group) * a.q_heads + g * a.group + r % a.group;
+__device__ __forceinline__ int64_t out_row(const KvqAttnArgs &a, int q0, int g, int r) {
+    return (int64_t)(q0 + r / a.group) * a.q_heads + g * a.group + r % a.group;
 }
 __device__ __forceinline__ float lse_of(float m, float l) {
     return l != 0.0f ? (m + log2f(l)) * 0.693147180559945f : -INFINITY;
@@ -744,7 +746,7 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void k_kvq_chunk(KvqAttnArgs a) {
         if (alone) {
             if (live) {
                 using O = ChunkOut<D>;
-                const int64_t to = out_row(a, seq, g, r);
+                const int64_t to = out_row(a, seq.q0, g, r);
 #pragma unroll
                 for (int q = 0; q < O::kQuads; ++q) {
                     const float v[4] = {o[O::u_of(q, 0)][O::i_of(q, 0)], o[O::u_of(q, 1)][O::i_of(q, 1)],
@@ -755,21 +757,24 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void k_kvq_chunk(KvqAttnArgs a) {
             }
         } else {
             const int slot = 2 * blockIdx.x + (first ? 0 : 1);
+            if (wave_live) {
 #pragma unroll
-            for (int u = 0; u < kMTiles; ++u)
+                for (int u = 0; u < kMTiles; ++u)
 #pragma unroll
-                for (int i = 0; i < 16; ++i) parts[slot].o[wave][16 * u + i][lane] = o[u][i];
-            if (half == 0) {
-                parts[slot].ml[wave][n][0] = m;
-                parts[slot].ml[wave][n][1] = l;
+                    for (int i = 0; i < 16; ++i) parts[slot].o[wave][16 * u + i][lane] = o[u][i];
+                if (half == 0) {
+                    parts[slot].ml[wave][n][0] = m;
+                    parts[slot].ml[wave][n][1] = l;
+                }
             }
             if (tid == 0 && pos == item_begin) {
                 const int64_t at = more * (each + 1), unit = item_end - 1;
                 ChunkSplit s{};
                 s.last = (int)(unit < at ? udiv(unit, each + 1) : more + udiv(unit - at, each));
                 s.slot = slot;
-                s.seq = b;
-                s.tile = rt;
+                s.q0 = seq.q0;
+                s.row = r0;
+                s.rows = r1 - r0;
                 s.head = g;
                 splits[blockIdx.x] = s;
             }
@@ -778,50 +783,130 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void k_kvq_chunk(KvqAttnArgs a) {
     }
 }
 
-// Joins the parts of the item that workgroup blockIdx.x of k_kvq_chunk began and did
-// not end, for the rows of one of its waves.
+// Joins the parts of the items that a workgroup of k_kvq_chunk, of `groups`, began and
+// did not end.  A task is the rows of one of that workgroup's waves; each of four waves
+// here takes a quarter of their dimensions.  Where there are few such items, of many
+// parts each (long caches), a task is one quarter, and of that the four waves take every
+// fourth part each: a wave by itself would wait for one after the other.  The first wave
+// adds up their sums, in their order.  The workgroups share the tasks out between them:
+// one for every task that there might be would take longer to start and end the idle
+// ones than the others take to work.  Measured with 8 heads of 128: 8 us where one
+// sequence of 48 rows has 32 parts an item (24 us by one wave for each quarter), 17.6 us
+// where items have two full parts (67 MB, 14 us at the rate of a copy).
+constexpr int kJoinWaves = 4;
 template <int GT, int D, int NW>
-__global__ __launch_bounds__(256) void k_kvq_chunk_join(KvqAttnArgs a) {
+__global__ __launch_bounds__(64 * kJoinWaves) void k_kvq_chunk_join(KvqAttnArgs a, int groups) {
     using O = ChunkOut<D>;
-    const ChunkSplit s = reinterpret_cast<const ChunkSplit *>(a.workspace)[blockIdx.x];
-    if (s.last < 0) return;
+    constexpr int kMine = O::kQuads / 4, kBatch = 2, kPer = kChunkMaxGroups / (64 * kJoinWaves);
+    __shared__ float s_v[kJoinWaves - 1][4 * kMine][64], s_ml[kJoinWaves - 1][64][2];
+    __shared__ int16_t s_items[kChunkMaxGroups];
+    __shared__ int s_count[kJoinWaves];
+    const ChunkSplit *splits = reinterpret_cast<const ChunkSplit *>(a.workspace);
     const ChunkPartial<GT, D, NW> *parts = reinterpret_cast<const ChunkPartial<GT, D, NW> *>(
         static_cast<const char *>(a.workspace) + kChunkMaxGroups * sizeof(ChunkSplit));
-    const int lane = threadIdx.x & 63, share = threadIdx.x >> 6, wave = blockIdx.y;
+    const int lane = threadIdx.x & 63, line = uniform((int)(threadIdx.x >> 6));
     const int n = lane & 31, half = lane >> 5;
-    const KvqSeq seq = kvq_seq(a, s.seq);
-    const int r = s.tile * 32 * NW + 32 * wave + n;
-    if (s.tile * 32 * NW + 32 * wave >= seq.len * a.group) return;
-    constexpr int kMine = O::kQuads / 4;
-    float v[kMine][4], m = kUnseen, l = 0.0f;
+
+    // the workgroups that began such an item
+    uint64_t has[kPer];
+    int count = 0;
 #pragma unroll
-    for (int q = 0; q < kMine; ++q)
+    for (int k = 0; k < kPer; ++k) {
+        const int w = 64 * (kPer * line + k) + lane;
+        has[k] = __ballot(w < groups && splits[min(w, groups - 1)].last >= 0);
+        count += __popcll(has[k]);
+    }
+    if (lane == 0) s_count[line] = count;
+    __syncthreads();
+    int items = 0, at = 0;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) v[q][k] = 0.0f;
-    for (int w = blockIdx.x; w <= s.last; ++w) {
-        const ChunkPartial<GT, D, NW> &p = parts[w == (int)blockIdx.x ? s.slot : 2 * w];
-        const float pm = p.ml[wave][n][0], pl = p.ml[wave][n][1];
-        const float top = fmaxf(m, pm), f0 = exp2_fast(m - top), f = pl * exp2_fast(pm - top);
-        m = top;
-        l = l * f0 + f;
+    for (int w = 0; w < kJoinWaves; ++w) {
+        at += w < line ? s_count[w] : 0;
+        items += s_count[w];
+    }
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) {
+        if (has[k] >> lane & 1) s_items[at + __popcll(has[k] & ((1ull << lane) - 1))] = (int16_t)(64 * (kPer * line + k) + lane);
+        at += __popcll(has[k]);
+    }
+
+    items = uniform(items);
+    const int lines = 4 * items < groups ? kJoinWaves : 1, tasks = items * NW * lines;
+    for (int task = blockIdx.x; task < tasks; task += gridDim.x) {
+        __syncthreads();  // s_items is written; the task before is done with the sums
+        const int at = task / lines, begin = uniform((int)s_items[at / NW]), wave = at % NW;
+        const int quarter = lines > 1 ? task % lines : line;
+        const ChunkSplit s = splits[begin];
+        if (32 * wave >= s.rows) continue;
+        float v[kMine][4], m = kUnseen, l = 0.0f;
 #pragma unroll
         for (int q = 0; q < kMine; ++q)
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                // the register's number, with `share` the only part that is not a constant
-                const int at = kMine * share + q;
-                v[q][k] = fmaf(p.o[wave][16 * O::u_of(at, k) + O::i_of(at, k)][lane], f, v[q][k] * f0);
-            }
-    }
-    const float inv = l != 0.0f ? 1.0f / l : 0.0f;
-    if (r >= seq.len * a.group) return;
-    const int64_t to = out_row(a, seq, s.head, r);
+            for (int k = 0; k < 4; ++k) v[q][k] = 0.0f;
+        const auto add = [&](const float (&o)[kMine][4], float pm, float pl) {
+            const float top = fmaxf(m, pm), f0 = exp2_fast(m - top), f = pl * exp2_fast(pm - top);
+            m = top;
+            l = l * f0 + f;
 #pragma unroll
-    for (int q = 0; q < kMine; ++q) {
-        const float x[4] = {v[q][0] * inv, v[q][1] * inv, v[q][2] * inv, v[q][3] * inv};
-        store_four<GT>(a, to, O::dim_of(kMine * share + q, half), D, x);
+            for (int q = 0; q < kMine; ++q)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) v[q][k] = fmaf(o[q][k], f, v[q][k] * f0);
+        };
+        for (int w = begin + (lines > 1 ? line : 0); w <= s.last; w += kBatch * lines) {
+            float o[kBatch][kMine][4], pm[kBatch], pl[kBatch];
+#pragma unroll
+            for (int t = 0; t < kBatch; ++t) {
+                // (past the last part the one at w again, with nothing of it)
+                const int at = w + t * lines <= s.last ? w + t * lines : w;
+                const ChunkPartial<GT, D, NW> &p = parts[at == begin ? s.slot : 2 * at];
+                pm[t] = p.ml[wave][n][0];
+                pl[t] = t == 0 || at != w ? p.ml[wave][n][1] : 0.0f;
+#pragma unroll
+                for (int q = 0; q < kMine; ++q)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        // the register's number, with `quarter` the only part that is not a constant
+                        const int x = kMine * quarter + q;
+                        o[t][q][k] = p.o[wave][16 * O::u_of(x, k) + O::i_of(x, k)][lane];
+                    }
+            }
+#pragma unroll
+            for (int t = 0; t < kBatch; ++t) add(o[t], pm[t], pl[t]);
+        }
+        if (lines > 1) {
+            if (line > 0) {
+#pragma unroll
+                for (int q = 0; q < kMine; ++q)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) s_v[line - 1][4 * q + k][lane] = v[q][k];
+                s_ml[line - 1][lane][0] = m;
+                s_ml[line - 1][lane][1] = l;
+            }
+            __syncthreads();
+            if (line > 0) continue;
+            // (a wave's sums are not divided by l: they enter with the weight 1)
+#pragma unroll
+            for (int w = 0; w < kJoinWaves - 1; ++w) {
+                const float pm = s_ml[w][lane][0], top = fmaxf(m, pm), f0 = exp2_fast(m - top), f = exp2_fast(pm - top);
+                m = top;
+                l = l * f0 + s_ml[w][lane][1] * f;
+#pragma unroll
+                for (int q = 0; q < kMine; ++q)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) v[q][k] = fmaf(s_v[w][4 * q + k][lane], f, v[q][k] * f0);
+            }
+        }
+        const float inv = l != 0.0f ? 1.0f / l : 0.0f;
+        if (32 * wave + n < s.rows) {
+            const int64_t to = out_row(a, s.q0, s.head, s.row + 32 * wave + n);
+#pragma unroll
+            for (int q = 0; q < kMine; ++q) {
+                const float x[4] = {v[q][0] * inv, v[q][1] * inv, v[q][2] * inv, v[q][3] * inv};
+                store_four<GT>(a, to, O::dim_of(kMine * quarter + q, half), D, x);
+            }
+            if (a.lse && quarter == 0 && half == 0) a.lse[to] = lse_of(m, l);
+        }
     }
-    if (a.lse && share == 0 && half == 0) a.lse[to] = lse_of(m, l);
 }
 
 }  // namespace onebit
