@@ -15,9 +15,15 @@
 // the codes (c - z) themselves, exact, and the scales are applied to scores and weights
 // in fp32, because an fp16 output would show those roundings.
 //
-// The work is one line of tiles, shared out and joined as in the step kernel, except
-// that a second small kernel joins the partial results (a workgroup's is too large to
-// be read back by one).
+// The work is one line of tiles, shared out as in the step kernel.  A second kernel
+// joins the partial results: a workgroup's has up to 133 KB, too much for the last
+// one of an item to read them all.
+//
+// Measured: 2048 new tokens over 32768, 32/8 heads of 128, bf16, 1240 us (0.86 PFLOP/s;
+// a library product of 8192^3 reaches 1.14, a bare loop of these products with their
+// operands from LDS and as many vector operations 1.09); first chunks of 1500 to 4000
+// tokens, 16 heads of 64, fp16, 170 us; 9 chunks of up to 700 tokens, 16/4 heads of 256,
+// 4 bits, cap and window, 240 us, bound by issue with one wave on each SIMD.
 #pragma once
 
 #include "kvq_attention.h"
