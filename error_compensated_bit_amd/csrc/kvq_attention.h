@@ -179,9 +179,18 @@ __device__ __forceinline__ int64_t uniform(int64_t v) {
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
 __device__ __forceinline__ float pow2(int k) { return __uint_as_float((uint32_t)(127 + k) << 23); }  // -126 <= k <= 127
 
-// softcap * tanh(s / softcap) in units of log2(e), from y = 2 log2(e) s / softcap
+// softcap * tanh(s / softcap) in units of log2(e), from y = 2 log2(e) s / softcap.  The
+// difference is off by 2^-21 of the cap, whatever the score: caps above 64 (kWideCap2 in
+// these units) take scores below an eighth of the cap from tanh's series, whose first
+// term left out is 2^-29 of the score.
+constexpr float kWideCap2 = 92.4f;
 __device__ __forceinline__ float capped(float y, float cap2) {
     return fmaf(-2.0f * cap2, __builtin_amdgcn_rcpf(exp2_fast(y) + 1.0f), cap2);
+}
+__device__ __forceinline__ float capped_wide(float y, float cap2) {
+    const float z = y * 0.346573590f, zz = z * z;
+    const float series = fmaf(zz, fmaf(zz, fmaf(zz, -17.0f / 315, 2.0f / 15), -1.0f / 3), 1.0f);
+    return fabsf(z) < 0.125f ? cap2 * (z * series) : capped(y, cap2);
 }
 
 // Largest power of two k with |s| 2^k < 2^7 for every value scale up to `top`.

@@ -127,7 +127,8 @@ extern "C" onebit_status_t kvq_attention(const void *q, onebit_dtype_t dtype, in
     if (need == 0) return ONEBIT_ERR_INVALID;
     if (max_pages < 0 || max_pages > (0x7fffffff - 2048) / cache->page || (batch > 1 && table_stride < max_pages))
         return ONEBIT_ERR_INVALID;
-    if (window < 0 || !(softcap >= 0.0) || !__builtin_isfinite((float)softcap) || !__builtin_isfinite((float)sm_scale))
+    // (what the kernels make of both stays far from fp32's ends)
+    if (window < 0 || !(softcap == 0.0 || (softcap >= 0x1p-64 && softcap <= 0x1p64)) || !(__builtin_fabs(sm_scale) <= 0x1p64))
         return ONEBIT_ERR_INVALID;
     if (batch == 0 || total_q == 0) return ONEBIT_OK;
     if (!q_offsets && total_q % batch) return ONEBIT_ERR_INVALID;

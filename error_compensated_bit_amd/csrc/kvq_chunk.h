@@ -23,7 +23,7 @@
 // a library product of 8192^3 reaches 1.14, a bare loop of these products with their
 // operands from LDS and as many vector operations 1.09); first chunks of 1500 to 4000
 // tokens, 16 heads of 64, fp16, 170 us; 9 chunks of up to 700 tokens, 16/4 heads of 256,
-// 4 bits, cap and window, 240 us, bound by issue with one wave on each SIMD.
+// 4 bits, cap and window, 244 us, bound by issue with one wave on each SIMD.
 #pragma once
 
 #include "kvq_attention.h"
@@ -544,8 +544,13 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void k_kvq_chunk(KvqAttnArgs a) {
             scale = qk;
             if (a.cap2 > 0.0f || !whole) {
                 if (a.cap2 > 0.0f) {
+                    if (a.cap2 > kWideCap2) {
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) x[i] = capped(x[i] * qk, a.cap2);
+                        for (int i = 0; i < 16; ++i) x[i] = capped_wide(x[i] * qk, a.cap2);
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) x[i] = capped(x[i] * qk, a.cap2);
+                    }
                     scale = 1.0f;
                 }
                 if (!whole) {

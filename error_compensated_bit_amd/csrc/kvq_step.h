@@ -349,7 +349,7 @@ __global__ __launch_bounds__(kStepBlock, NT == 1 && D <= 128 ? 3 : 2) void k_kvq
 #pragma unroll
                 for (int k = 0; k < 8; ++k) {
                     float y = acc[nt][k >> 2][k & 3] * kscale[k >> 2][k & 3] * qs[nt];
-                    if (a.cap2 > 0.0f) y = capped(y, a.cap2);
+                    if (a.cap2 > 0.0f) y = a.cap2 > kWideCap2 ? capped_wide(y, a.cap2) : capped(y, a.cap2);
                     if (!whole) {
                         const int t = j + 16 * (k >> 2) + 4 * c + (k & 3);
                         if (!(page_ok[k >> 2] && t >= lo[nt] && t < hi[nt])) y = kNone;

@@ -496,7 +496,9 @@ onebit_status_t kvq_dequantize(const kvq_cache_t *cache, const int64_t *slots, i
  * [0, n_pages) counts as not attended to, offsets are clamped to 0 .. total_q.  What
  * the cache holds in positions that are not attended to has no influence, whatever its
  * bits.  q_heads a multiple of kv_heads; total_q * q_heads and max_pages * page
- * below 2^31 - 2048; sm_scale finite.
+ * below 2^31 - 2048; sm_scale from -2^64 to 2^64; softcap 0 or from 2^-64 to 2^64.  Scores
+ * are formed in binary32: max |q| * |sm_scale| (with a softcap, twice that over it) is to
+ * stay below 2^100, else rows may come out NaN.
  * workspace: kvq_attention_workspace_bytes bytes (on the device that is current), 16-byte
  * aligned, zeroed once before its first use (onebit_workspace_init); every completed
  * call leaves it ready for the next one, of any sizes it is large enough for.  Calls

@@ -56,7 +56,8 @@ def attention(q, pools, table, kv_lens, *, bits, scale, q_offsets=None, softcap=
         exact as if each were 1024 (8 bits) or 64 (4 bits) in place of c - z, that is R = 1024 or 64
         scales in place of k_d: (D + 8) 2^-24 R scale_j sum_d |q_d| each.  exp2's argument is
         rounded at the size of the score itself and exp2 is good to an ulp: 2^-22 (|s| + 1); a
-        capped score is off by 2^-21 cap.  An error e of every score moves each weight and their sum
+        capped score is off by 2^-21 cap, and for caps above 64 by 2^-21 of the score itself below an
+        eighth of the cap (so by 2^-18 |s| at most).  An error e of every score moves each weight and their sum
         by e: 2 e A;
       - the sums over n terms in fp32, of codes too: (n + 64) 2^-24 (A + R sum_j softmax_j scale_j),
         twice.
@@ -112,8 +113,8 @@ def attention(q, pools, table, kv_lens, *, bits, scale, q_offsets=None, softcap=
                     off = off + abs(scale) * (2.0 ** -10 * (x.abs() @ k.abs().T) +
                                               2.0 ** -14 * k_top * x.abs().sum(1, keepdim=True))
                 if softcap:
+                    off = off + 2.0 ** -21 * (softcap if softcap <= 64 else (8 * s.abs()).clamp(max=softcap))
                     s = softcap * torch.tanh(s / softcap)
-                    off = off + 2.0 ** -21 * softcap
                 s = s.masked_fill(~keep, -math.inf)
                 some = keep.any(1)
                 peak = torch.where(some, s.amax(1), torch.zeros(m, dtype=torch.float64))

@@ -249,6 +249,19 @@ def test_windows_and_caps(window, softcap, bits, dim, page):
                                       softcap=softcap, window=window), BF16)
 
 
+@pytest.mark.parametrize("softcap", [2.0 ** -64, 64.0, 65.0, 100.0, 5e4, 1e9, 2.0 ** 64])
+@pytest.mark.parametrize("bits,dtype", [(8, F16), (4, BF16), (8, BF16)])
+def test_caps_far_from_the_scores(softcap, bits, dtype):
+    """A cap far above the scores leaves them as they are (the difference that tanh's formula ends in
+    does not), one far below makes them all alike; scores from 0 to beyond an eighth of the cap."""
+    qs, ks = [1, 5, 200, 33, 1], [700, 300, 400, 70, 2500]
+    g = gen("caps", softcap, bits, dtype)
+    q, pools, table, lens, offs = make(g, qs, ks, 4, 2, 128, 32, bits, dtype)
+    q[7:40] = 0
+    got, lse = attend(q, pools, table, lens, bits, q_offsets=offs, softcap=softcap, scale=0.5)
+    check(got, lse, kvq_ref.attention(q, pools, table, lens, bits=bits, scale=0.5, q_offsets=offs, softcap=softcap), dtype)
+
+
 @pytest.mark.parametrize("q_len", [1, 2, 5, 9, 48])
 @pytest.mark.parametrize("bits", [4, 8])
 def test_rows_that_attend_to_nothing(q_len, bits):

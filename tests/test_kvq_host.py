@@ -95,6 +95,7 @@ def test_read_refusals(kw, status):
     (dict(total=2 ** 31, hq=2, ws_bytes=1 << 40), INV), (dict(total=2 ** 30, ws_bytes=1 << 40), INV),
     (dict(max_pages=-1), INV), (dict(max_pages=2 ** 27), INV), (dict(max_pages=3), INV),   # rows closer than 3
     (dict(window=-1), INV), (dict(cap=-1.0), INV), (dict(cap=math.nan), INV), (dict(cap=math.inf), INV),
+    (dict(cap=2.0 ** 65), INV), (dict(cap=2.0 ** -65), INV), (dict(scale=-2.0 ** 65), INV),
     (dict(cap=1e39), INV), (dict(scale=math.nan), INV), (dict(scale=math.inf), INV), (dict(scale=1e39), INV),
     (dict(q=None), INV), (dict(kv=None), INV), (dict(out=None), INV), (dict(table=None), INV), (dict(ws=None), INV),
     (dict(ws_bytes=0), INV), (dict(q=A + 8), ALIGN), (dict(out=A + 8), ALIGN), (dict(ws=A + 8), ALIGN),
