@@ -565,6 +565,10 @@ def kvq_attention(q, k_codes, k_scales, v_codes, v_scales, block_table, kv_lens,
         raise ValueError(f"q_offsets must be [{batch + 1}]")
     if lse is not None and list(lse.shape) != [total, q_heads]:
         raise ValueError(f"lse must be [{total}, {q_heads}]")
+    if not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    if abs(window) >= 2 ** 31:                 # (would be cut to 32 bits on its way)
+        raise ValueError(f"window must be from 0 to 2^31 - 1, got {window}")
     _kvq_call("kvq_attention", device, stream, q.data_ptr(), _dtype_code(q), total, q_heads, qt, qh,
               None if q_offsets is None else _dense(q_offsets, torch.int32, "q_offsets"),
               _dense(kv_lens, torch.int32, "kv_lens"), batch, block_table.data_ptr(), max_pages,

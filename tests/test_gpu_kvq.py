@@ -790,6 +790,7 @@ def test_binding_refusals_with_device_tensors():
         (ValueError, dict(kw=dict(q_offsets=torch.zeros(2, dtype=torch.int32, device=DEV)))),
         (ValueError, dict(kw=dict(lse=torch.zeros(2, 2, device=DEV)))),
         (ob.OnebitError, dict(kw=dict(window=-1))), (ob.OnebitError, dict(kw=dict(softcap=-1.0))),
+        (ValueError, dict(kw=dict(window=2 ** 32 + 1))), (ValueError, dict(kw=dict(workspace=ws[:64].expand(ws.numel(), 64)))),
         (ob.OnebitError, dict(kw=dict(workspace=ws[:16]))), (ob.OnebitError, dict(q=q.float(), out=q.float())),
         (ob.OnebitError, dict(q=torch.zeros(2, 3, 64, dtype=BF16, device=DEV),
                               out=torch.zeros(2, 3, 64, dtype=BF16, device=DEV))),
