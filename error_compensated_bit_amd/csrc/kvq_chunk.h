@@ -628,10 +628,22 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void k_kvq_chunk(KvqAttnArgs a) {
         // step's scores and the last step's values; in a tile's first step the tile after next is
         // expanded, too.  Four tiles' places in LDS: the one before this, whose last values are
         // still to be multiplied, this and the next one, and the one being expanded.
+        // The last values of a wave, of tile `it`.  (No maximum has moved since their weights were computed.)
+        const auto last_values = [&](int it) {
+#pragma unroll
+            for (int x = 0; x < kPv; ++x) mul_v(kSubs == 1 ? 1 : (kSubs - 1) & 1, x, read_v(it & 3, kSubs - 1, x));
+        };
+        // (a wave whose rows attend to nothing further on only expands: above a diagonal of 256 tokens)
+        const int wave_hi = wave_live ? kvq_hi(seq, wt1) : 0;
+        bool working = wave_live;
         for (int it = 0; it < count; ++it) {
             const int j = from + it * kTile, buf = it & 3, after = (it + 1) & 3, fresh = (it + 2) & 3;
             if (it > 0) __syncthreads();
-            if (!wave_live) {
+            if (working && it > 0 && j >= wave_hi) {
+                last_values(it - 1);
+                working = false;
+            }
+            if (!working) {
                 expand_begin(stage, j + 2 * kTile);
 #pragma unroll
                 for (int x = 0; x < kPieces; ++x) expand_piece(stage, fresh, x);
@@ -739,12 +751,7 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void k_kvq_chunk(KvqAttnArgs a) {
                 }
             }
         }
-        if (count > 0 && wave_live) {
-            const int vb = (count - 1) & 3;
-            // (no maximum has moved since these weights were computed)
-#pragma unroll
-            for (int x = 0; x < kPv; ++x) mul_v(kSubs == 1 ? 1 : (kSubs - 1) & 1, x, read_v(vb, kSubs - 1, x));
-        }
+        if (count > 0 && working) last_values(count - 1);
 
         // ---- results
         l += __shfl_xor(l, 32, 64);
