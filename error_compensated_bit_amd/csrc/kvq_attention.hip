@@ -34,7 +34,7 @@ constexpr int chunk_waves(int dim) { return dim == 256 ? 4 : 8; }
 // The step kernel's counters, then the partial results of either kernel (one runs after
 // the other).
 static size_t step_bytes(int dim) {
-    return (size_t)step_groups() * 2 * (dim == 256 ? 16 : 32) * (dim + 2) * sizeof(float);
+    return (size_t)step_groups() * 2 * (dim == 128 ? 32 : 16) * (dim + 2) * sizeof(float);
 }
 static size_t chunk_bytes(int dim) {
     return kChunkMaxGroups * sizeof(ChunkSplit) +
@@ -61,11 +61,21 @@ static KvqAttnArgs slice(const KvqAttnArgs &a, int b, int count) {
 
 template <int GT, int D, int BITS>
 static void launch(KvqAttnArgs a, hipStream_t s) {
-    constexpr int kWide = D == 256 ? 1 : 2, kWaves = chunk_waves(D);
-    a.max_rows = 32;
+    constexpr int kWide = D == 128 ? 2 : 1, kWaves = chunk_waves(D);
+    // Measured with 48 rows against the chunk kernel (us, 8 x 4096 tokens / 32 x 16384, 8 heads):
+    // bf16 heads of 64 25 : 41 / 217 : 291, of 128 39 : 55 / 372 : 428, fp16 39 : 72 / 396 : 607; one
+    // sequence of 16384 38 : 37; with 64 rows and bf16 56 : 55 / 606 : 428.
+    a.max_rows = 48;
     const int64_t rows = (int64_t)a.q_uniform * a.group;  // of every sequence, where that is known
     if (a.q_offsets || rows <= a.max_rows) {
-        const bool wide = kWide == 2 && (a.group > 16 || (!a.q_offsets && rows > 16));
+        // 17 to 32 rows at once read the cache once, but leave room for fewer workgroups and join more
+        // slowly.  That pays with heads of 128, where a second reading would come from memory and not
+        // from the 256 MB cache in front of it (as far as the tables tell): 32 rows, 8 heads, 32 x 16384
+        // tokens 266 : 327 us, but 32 x 2000 63 : 57, 8 x 4096 60 : 39, 1 x 16384 102 : 47.  With heads
+        // of 64 it is 180 : 181 at the best.
+        const int64_t most = a.q_offsets ? a.group : rows;
+        const bool wide = kWide == 2 && most > 16 && most <= 32 &&
+                          (double)a.batch * a.c.heads * a.max_tokens * (D * BITS / 4 + 8) > 0x1p28;
         for (int b = 0; b < a.batch; b += kStepSeqs) {
             const KvqAttnArgs x = slice(a, b, kStepSeqs);
             if (wide)

@@ -22,7 +22,7 @@
 // Measured: 2048 new tokens over 32768, 32/8 heads of 128, bf16, 1240 us (0.86 PFLOP/s;
 // a library product of 8192^3 reaches 1.14, a bare loop of these products with their
 // operands from LDS and as many vector operations 1.09); first chunks of 1500 to 4000
-// tokens, 16 heads of 64, fp16, 170 us; 9 chunks of up to 700 tokens, 16/4 heads of 256,
+// tokens, 16 heads of 64, fp16, 168 us; 9 chunks of up to 700 tokens, 16/4 heads of 256,
 // 4 bits, cap and window, 244 us, bound by issue with one wave on each SIMD.
 #pragma once
 
@@ -73,13 +73,13 @@ struct ChunkShape {
 constexpr int kAhead = 4;
 // A value that a piece computes for later: the compiler would move its computation there.
 __device__ __forceinline__ void pin(uint32_t &v) { asm volatile("" : "+v"(v)); }
-// The first reads are issued (read_first) well before the products they feed.
 // The largest of three, NaN if one is: one instruction, where fmaxf costs one more for
 // each operand that might be a signalling NaN.  (A row with a NaN score comes out NaN
 // whatever its running maximum.)
 __device__ __forceinline__ float max3(float a, float b, float c) {
     return __builtin_elementwise_maximum(__builtin_elementwise_maximum(a, b), c);
 }
+// The first reads are issued well before the products they feed.
 template <int N, typename Read>
 __device__ __forceinline__ void read_first(f16x8_v (&f)[kAhead], Read read) {
 #pragma unroll

@@ -61,7 +61,7 @@ def attention(q, pools, table, kv_lens, *, bits, scale, q_offsets=None, softcap=
         by e: 2 e A;
       - the sums over n terms in fp32, of codes too: (n + 64) 2^-24 (A + R sum_j softmax_j scale_j),
         twice.
-    Chunks (more than 32 rows, tokens x heads of a cache head) of bf16 take the rows as fp16: the
+    Chunks (more than 48 rows, tokens x heads of a cache head) of bf16 take the rows as fp16: the
     scale and the product are each rounded once, 2^-10 of a key or value, and what fp16's range cuts
     off is below 2^-14 of the largest scale: 2^-10 sum_d |q_d k_d| + 2^-14 max(scale) sum_d |q_d| for
     a score, 2^-10 A + 2^-14 max(scale) for an output.
@@ -107,7 +107,7 @@ def attention(q, pools, table, kv_lens, *, bits, scale, q_offsets=None, softcap=
                 s = scale * (x @ k.T)
                 size = abs(scale) * reach * x.abs().sum(1, keepdim=True) * ks.double().abs()
                 off = (dim + 8) * 2.0 ** -24 * size + 2.0 ** -22 * (s.abs() + 1)
-                rounded = q.dtype == torch.bfloat16 and m * group > 32
+                rounded = q.dtype == torch.bfloat16 and m * group > 48
                 k_top, v_top = (float(torch.nan_to_num(t, posinf=0.0).abs().max()) for t in (ks, vs))
                 if rounded:
                     off = off + abs(scale) * (2.0 ** -10 * (x.abs() @ k.abs().T) +

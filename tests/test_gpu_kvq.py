@@ -518,6 +518,34 @@ def test_more_query_heads_of_a_cache_head_than_a_tile_has_rows(hq, heads, dim):
     check(got, lse, kvq_ref.attention(q, pools, table, lens, bits=8, scale=dim ** -0.5, q_offsets=offs), BF16)
 
 
+@pytest.mark.parametrize("hq,heads,dim", [(3, 3, 64), (2, 1, 128), (1, 1, 256)])
+@pytest.mark.parametrize("rows", [16, 18, 32, 34, 48, 50, 64])
+@pytest.mark.parametrize("pages", [40, 70000])
+@pytest.mark.parametrize("ragged", [False, True])
+def test_row_counts_at_the_kernels_boundaries(hq, heads, dim, rows, pages, ragged):
+    """Also under a block table for far more tokens than there are."""
+    m = rows * heads // hq
+    g = gen("rows", hq, dim, rows, pages)
+    q, pools, table, lens, offs = make(g, [m] * 3, [m, 700, 333], hq, heads, dim, 16, 8, BF16)
+    wide = torch.full((3, max(pages, table.shape[1])), -1, dtype=torch.int32)
+    wide[:, :table.shape[1]] = table
+    got, lse = attend(q, pools, wide, lens, 8, q_offsets=offs if ragged else None)
+    check(got, lse, kvq_ref.attention(q, pools, table, lens, bits=8, scale=dim ** -0.5), BF16)
+
+
+@pytest.mark.parametrize("group", [17, 32, 33, 48, 49])
+@pytest.mark.parametrize("pages", [40, 70000])
+@pytest.mark.parametrize("ragged", [False, True])
+@pytest.mark.parametrize("dtype", [BF16, F16])
+def test_groups_at_the_kernels_boundaries(group, pages, ragged, dtype):
+    g = gen("groups", group, pages)
+    q, pools, table, lens, offs = make(g, [1] * 5, [1, 2000, 40, 0, 333], 2 * group, 2, 128, 16, 4, dtype)
+    wide = torch.full((5, max(pages, table.shape[1])), -1, dtype=torch.int32)
+    wide[:, :table.shape[1]] = table
+    got, lse = attend(q, pools, wide, lens, 4, q_offsets=offs if ragged else None)
+    check(got, lse, kvq_ref.attention(q, pools, table, lens, bits=4, scale=128 ** -0.5), dtype)
+
+
 @pytest.mark.parametrize("n,q_len", [(1024, 1), (1025, 1), (2100, 2), (512, 40), (1300, 33)])
 def test_more_sequences_than_a_launch_takes(n, q_len):
     g = gen("launches", n)
