@@ -328,7 +328,11 @@ __global__ __launch_bounds__(kStepBlock, NT == 1 && D <= 128 ? 3 : 2) void k_kvq
             }
             const bool whole = j >= all_lo && j + 32 <= all_hi && ok[0] && ok[1];
             const bool page_ok[2] = {ok[0], ok[1]};
-            const float kscale[2][4] = {{ks[0].x, ks[0].y, ks[0].z, ks[0].w}, {ks[1].x, ks[1].y, ks[1].z, ks[1].w}};
+            // (an infinite scale becomes NaN here: the score of its token may not come out -inf, of weight 0,
+            // nor go under a cap)
+            float kscale[2][4] = {{ks[0].x, ks[0].y, ks[0].z, ks[0].w}, {ks[1].x, ks[1].y, ks[1].z, ks[1].w}};
+#pragma unroll
+            for (int k = 0; k < 8; ++k) kscale[k >> 2][k & 3] = fmaf(kscale[k >> 2][k & 3], 0.0f, kscale[k >> 2][k & 3]);
             // the next tile's keys are on their way from here on (behind the last tile: of rows
             // that exist and are not used)
 #pragma unroll
