@@ -213,7 +213,6 @@ __global__ __launch_bounds__(kStepBlock, NT == 1 && D <= 128 ? 3 : 2) void k_kvq
         // the stretch's tokens that some row of the tile attends to
         const int from = max(base + (int)(pos - item_begin) * kStepUnit, kvq_lo(a, seq, t0) & ~31);
         const int to = (int)min((int64_t)kvq_hi(seq, t1), base + (seg_end - item_begin) * kStepUnit);
-        const int some_lo = kvq_lo(a, seq, t0);  // tokens in front of it are attended to by no row
         // tokens that all rows attend to
         const int all_lo = kvq_lo(a, seq, t1), all_hi = kvq_hi(seq, t0);
 
@@ -273,8 +272,15 @@ __global__ __launch_bounds__(kStepBlock, NT == 1 && D <= 128 ? 3 : 2) void k_kvq
 #pragma unroll
             for (int u = 0; u < T::kDims; ++u) o[nt][u] = (f32x4_v){0.0f, 0.0f, 0.0f, 0.0f};
         }
-        int kv_exp = 126;                    // value scales are taken times 2^kv_exp
-        float v_top = 0.0f;                  // the largest the exponent was chosen for
+        // A row's value scales are taken times 2^kv_exp, chosen for the largest that the row itself
+        // attends to: what other rows of the tile attend to must not decide what fp16 loses of its weights.
+        int kv_exp[NT];
+        float v_top[NT];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            kv_exp[nt] = 126;
+            v_top[nt] = 0.0f;
+        }
         const int32_t *table = a.table + (int64_t)b * a.table_stride;
         // page number of token j, and the cache row of token j (a multiple of 16); without branches,
         // where the compiler would wait for all loads under way.  Tokens behind the table's end
@@ -328,6 +334,10 @@ __global__ __launch_bounds__(kStepBlock, NT == 1 && D <= 128 ? 3 : 2) void k_kvq
             }
             const bool whole = j >= all_lo && j + 32 <= all_hi && ok[0] && ok[1];
             const bool page_ok[2] = {ok[0], ok[1]};
+            const auto attends = [&](int nt, int k) {  // to the lane's token k
+                const int t = j + 16 * (k >> 2) + 4 * c + (k & 3);
+                return page_ok[k >> 2] && t >= lo[nt] && t < hi[nt];
+            };
             // (an infinite scale becomes NaN here: the score of its token may not come out -inf, of weight 0,
             // nor go under a cap)
             float kscale[2][4] = {{ks[0].x, ks[0].y, ks[0].z, ks[0].w}, {ks[1].x, ks[1].y, ks[1].z, ks[1].w}};
@@ -354,10 +364,7 @@ __global__ __launch_bounds__(kStepBlock, NT == 1 && D <= 128 ? 3 : 2) void k_kvq
                 for (int k = 0; k < 8; ++k) {
                     float y = acc[nt][k >> 2][k & 3] * kscale[k >> 2][k & 3] * qs[nt];
                     if (a.cap2 > 0.0f) y = a.cap2 > kWideCap2 ? capped_wide(y, a.cap2) : capped(y, a.cap2);
-                    if (!whole) {
-                        const int t = j + 16 * (k >> 2) + 4 * c + (k & 3);
-                        if (!(page_ok[k >> 2] && t >= lo[nt] && t < hi[nt])) y = kNone;
-                    }
+                    if (!whole && !attends(nt, k)) y = kNone;
                     x[nt][k] = y;
                     top = fmaxf(top, y);
                 }
@@ -369,58 +376,65 @@ __global__ __launch_bounds__(kStepBlock, NT == 1 && D <= 128 ? 3 : 2) void k_kvq
                     float top = x[nt][0];
 #pragma unroll
                     for (int k = 1; k < 8; ++k) top = fmaxf(top, x[nt][k]);
-                    top = fmaxf(m[nt], over_quarters_max(top));
-                    const float f = exp2_fast(m[nt] - top);
-                    m[nt] = top;
+                    top = over_quarters_max(top);
+                    // (each row by its own scores: its roundings do not depend on the other rows')
+                    const float f = top > m[nt] + kSlack ? exp2_fast(m[nt] - top) : 1.0f;
+                    m[nt] = top > m[nt] + kSlack ? top : m[nt];
                     l[nt] *= f;
 #pragma unroll
                     for (int u = 0; u < T::kDims; ++u) o[nt][u] *= f;
                 }
             }
-            float vscale[2][4] = {{vs[0].x, vs[0].y, vs[0].z, vs[0].w}, {vs[1].x, vs[1].y, vs[1].z, vs[1].w}};
-            if (!whole) {
-                // rows that nobody attends to may hold anything
-#pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    const int t = j + 16 * (k >> 2) + 4 * c + (k & 3);
-                    if (!(page_ok[k >> 2] && t >= some_lo && t < to)) vscale[k >> 2][k & 3] = 0.0f;
-                }
-            }
-            float v_new = 0.0f;  // an infinite scale of one row must not set the others' range
+            const float vscale[2][4] = {{vs[0].x, vs[0].y, vs[0].z, vs[0].w}, {vs[1].x, vs[1].y, vs[1].z, vs[1].w}};
+            float v_size[8], v_new[NT];  // an infinite scale of one token must not set the others' range
+            bool rise = false;
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
                 const float v = fabsf(vscale[k >> 2][k & 3]);
-                v_new = fmaxf(v_new, v < INFINITY ? v : 0.0f);
+                v_size[k] = v < INFINITY ? v : 0.0f;
             }
-            if (__any(v_new > v_top)) {
-                v_top = fmaxf(v_top, over_quarters_max(v_new));
-                const int e = value_exponent(v_top);
+            if (whole) {
+                float v = v_size[0];
+#pragma unroll
+                for (int k = 1; k < 8; ++k) v = fmaxf(v, v_size[k]);
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) v_new[nt] = v;
+            } else {
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
+                    v_new[nt] = 0.0f;
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) v_new[nt] = fmaxf(v_new[nt], attends(nt, k) ? v_size[k] : 0.0f);
+                }
+            }
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) rise |= v_new[nt] > v_top[nt];
+            if (__any(rise)) {
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    v_top[nt] = fmaxf(v_top[nt], over_quarters_max(v_new[nt]));
+                    const int e = value_exponent(v_top[nt]);
 #pragma unroll
                     for (int u = 0; u < T::kDims; ++u)
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) o[nt][u][i] = ldexpf(o[nt][u][i], e - kv_exp);
+                        for (int i = 0; i < 4; ++i) o[nt][u][i] = ldexpf(o[nt][u][i], e - kv_exp[nt]);
+                    kv_exp[nt] = e;
                 }
-                kv_exp = e;
             }
-            const float vf = pow2(kv_exp);
-#pragma unroll
-            for (int k = 0; k < 8; ++k) vscale[k >> 2][k & 3] *= vf;
             f16x8_v pf[NT], pl[NT];
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
                 uint32_t pw[4], lw[4];
+                const float vf = pow2(kv_exp[nt]);
 #pragma unroll
                 for (int k = 0; k < 8; k += 2) {
                     float e[2], p[2];
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
                         e[i] = exp2_fast(x[nt][k + i] - m[nt]);
-                        p[i] = e[i] * vscale[k >> 2][(k & 3) + i];
-                        if (!whole) {
-                            const int t = j + 16 * (k >> 2) + 4 * c + (k & 3) + i;
-                            const bool in = page_ok[k >> 2] && t >= lo[nt] && t < hi[nt];
+                        p[i] = e[i] * (vscale[k >> 2][(k & 3) + i] * vf);
+                        if (!whole) {  // (tokens that the row does not attend to may hold anything)
+                            const bool in = attends(nt, k + i);
                             e[i] = in ? e[i] : 0.0f;
                             p[i] = in ? p[i] : 0.0f;
                         }
@@ -476,7 +490,7 @@ __global__ __launch_bounds__(kStepBlock, NT == 1 && D <= 128 ? 3 : 2) void k_kvq
             for (int u = 0; u < T::kDims; ++u) {
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    o[nt][u][i] = ldexpf(o[nt][u][i] * f, kUnitShift - kv_exp);
+                    o[nt][u][i] = ldexpf(o[nt][u][i] * f, kUnitShift - kv_exp[nt]);
                 }
                 *reinterpret_cast<f32x4_v *>(dst + 16 * u) = o[nt][u];
             }
