@@ -9,11 +9,13 @@
 // O^T = V^T P^T: as in the step kernel, a query row stays in its lane from the scores
 // to the output.
 //
-// For bf16 the rows are expanded to (c - z) scale 2^k, rounded to fp16: one step in
-// 2^11 of a value, where a code of 8 bits is one in 2^8 of the row's largest.  Then the
-// scores need one fused operation and one exponential each.  For fp16 the operands are
-// the codes (c - z) themselves, exact, and the scales are applied to scores and weights
-// in fp32, because an fp16 output would show those roundings.
+// Keys are expanded to the codes (c - z) themselves, exact, and their scales are applied to
+// the scores in fp32: a scale rounded to fp16 moves all of a token's score by up to one part in
+// 2^11, a quarter of a weight where scores are around 500, and saves nothing (2048 tokens over
+// 32768, bf16: heads of 128 1234 us so, 1223 exact; 64 399 : 409; 256 440 : 444).  Values likewise
+// for fp16 outputs.  For bf16 they are expanded to (c - z) scale 2^k, rounded to fp16: one step in
+// 2^11 of a value, where a code of 8 bits is one in 2^8 of the row's largest and the output
+// one in 2^8.  (Exact they would cost heads of 64 another 14%, of 128 10%, of 256 6%.)
 //
 // The work is one line of tiles, shared out as in the step kernel.  A second kernel
 // joins the partial results: a workgroup's has up to 133 KB, too much for the last
@@ -184,11 +186,10 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void k_kvq_chunk(KvqAttnArgs a) {
     using S = ChunkShape<GT, D, BITS, NW>;
     constexpr bool kExact = S::kExact;
     constexpr int kTile = S::kTile, kWide = S::kWide, kMTiles = D / 32, kSteps = D / 16;
-    constexpr int kOperandShift = kExact ? kUnitShift : kCodeShift<BITS>;  // an operand is 2^-that of what it stands for
-    constexpr float kExactScale = kUnitScale<BITS>;
+    constexpr int kValShift = kExact ? kUnitShift : kCodeShift<BITS>;  // an operand of values is 2^-that of what it stands for
     __shared__ _Float16 s_k[4][kTile][S::kKeyRow];
     __shared__ _Float16 s_v[4][D][S::kValRow];
-    __shared__ float s_ks[4][kExact ? kTile : 1], s_vs[4][kExact ? kTile : 1];
+    __shared__ float s_ks[4][kTile], s_vs[4][kExact ? kTile : 1];
     __shared__ int64_t s_pre[kChunkSeqs + 1];
     __shared__ int64_t s_scan[NW];
     const int tid = threadIdx.x, lane = tid & 63, wave = uniform((int)(tid >> 6));
@@ -326,7 +327,7 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void k_kvq_chunk(KvqAttnArgs a) {
                 }
                 qf[s] = query_operand<BITS>(f, up);
             }
-            qs = ldexpf(a.scale2, kOperandShift - kq);
+            qs = ldexpf(a.scale2, kUnitShift - kq);
             if (a.cap2 > 0.0f) qs *= a.cap_scale;
         };
 
@@ -421,12 +422,12 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void k_kvq_chunk(KvqAttnArgs a) {
             load_pages(pages0, from);
             load_pages(pages1, from + kTile);
         }
-        // exponents of the scales: of the tile in LDS, and of the one being expanded
-        float k_top = 0.0f, v_top = 0.0f;
-        int k_exp_next = 126, v_exp_next = 126;
-        float x_ks, x_kv, x_s4[4], kf, vf;  // scales of the tile being expanded, and their powers of two
+        // exponent of the value scales of the tile being expanded
+        float v_top = 0.0f;
+        int v_exp_next = 126;
+        float x_ks, x_kv, x_s4[4], vf;  // scales of the tile being expanded, and the values' power of two
         const auto expand_begin = [&](const Stage &s, int j) {
-            float kt = 0.0f, vt = 0.0f;
+            float vt = 0.0f;
             bool plain = true;  // every token is attended to by some row and has finite scales
 #pragma unroll
             for (int i = 0; i < kWatch; ++i) {
@@ -434,21 +435,14 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void k_kvq_chunk(KvqAttnArgs a) {
                 const bool in = s.w_ok[i] && x < INFINITY && y < INFINITY;
                 there_next[i] = __ballot(s.w_there[i]);
                 plain = plain && __ballot(in) == ~0ull;
-                kt = fmaxf(kt, in ? x : 0.0f);
                 vt = fmaxf(vt, in ? y : 0.0f);
             }
-            if (__any(kt > k_top || vt > v_top)) {
+            if (__any(vt > v_top)) {
 #pragma unroll
-                for (int d = 32; d >= 1; d >>= 1) {
-                    kt = fmaxf(kt, __shfl_xor(kt, d, 64));
-                    vt = fmaxf(vt, __shfl_xor(vt, d, 64));
-                }
-                k_top = fmaxf(k_top, kt);
+                for (int d = 32; d >= 1; d >>= 1) vt = fmaxf(vt, __shfl_xor(vt, d, 64));
                 v_top = fmaxf(v_top, vt);
-                k_exp_next = uniform(scale_exponent<BITS>(k_top));
                 v_exp_next = uniform(kExact ? value_exponent(v_top) : scale_exponent<BITS>(v_top));
             }
-            kf = pow2(k_exp_next);
             vf = pow2(v_exp_next);
             x_ks = s.ks;
             x_kv = s.kv;
@@ -473,21 +467,20 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void k_kvq_chunk(KvqAttnArgs a) {
         constexpr int kPieces = 5 * kWide;
         const auto expand_piece = [&](const Stage &s, int buf, int piece) {
             if (piece < kWide) {
-                const f16x2_v scale = splat16(kExact ? kExactScale : x_ks * kf);
                 uint4 x[2];
-                expand16<BITS>(s.kw[piece], scale, scale * (_Float16)-0x1p-17f, x);
+                expand16<BITS>(s.kw[piece], splat16(kUnitScale<BITS>), splat16(-kUnitOffset<BITS>), x);
                 uint4 *dst = reinterpret_cast<uint4 *>(&s_k[buf][first_token + k_token][k_dim + 16 * piece]);
                 dst[0] = x[0];
                 dst[1] = x[1];
-                if (kExact && k_dim == 0 && piece == 0) {
+                if (k_dim == 0 && piece == 0) {
                     s_ks[buf][first_token + k_token] = x_ks;
-                    s_vs[buf][first_token + k_token] = x_kv * vf;
+                    if (kExact) s_vs[buf][first_token + k_token] = x_kv * vf;
                 }
             } else {
                 const int d = piece - kWide, w = BITS == 8 ? d / 4 : 0;
                 f16x2_v s2[2];
 #pragma unroll
-                for (int t = 0; t < 4; ++t) s2[t >> 1][t & 1] = (_Float16)(kExact ? kExactScale : x_s4[t] * vf);
+                for (int t = 0; t < 4; ++t) s2[t >> 1][t & 1] = (_Float16)(kExact ? kUnitScale<BITS> : x_s4[t] * vf);
                 // four tokens are eight bytes; of each 16 tokens, those that one half of a wave
                 // multiplies lie together
                 const int quad = (first_token + v_token) / 4;
@@ -505,7 +498,7 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void k_kvq_chunk(KvqAttnArgs a) {
         float f_grow = 1.0f, scale = 0.0f;
         bool grow = false;
         int v_exp = 126;                       // of what the outputs have summed
-        int k_exps[3], v_exps[3];              // of tiles it, it + 1, it + 2
+        int v_exps[3];                         // of tiles it, it + 1, it + 2
         uint64_t theres[2][kWatch];            // of tiles it, it + 1
 #pragma unroll
         for (int u = 0; u < kMTiles; ++u)
@@ -535,11 +528,11 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void k_kvq_chunk(KvqAttnArgs a) {
 #pragma unroll
             for (int i = 0; i < 16; ++i) x[i] = 0.0f;
         };
-        // scores of step `sub` of the tile in `buf`, whose first token is js: scales, cap and mask,
-        // and the running maximum.  `top` is the row's largest raw score where that is all there is to do.
-        const auto settle = [&](f32x16_v &x, float top, int buf, int sub, int js, int k_exp, const uint64_t (&here2)[kWatch]) {
+        // scores of step `sub` of a tile, whose first token is js: scale, cap and mask, and the
+        // running maximum.  `top` is the row's largest raw score where that is all there is to do.
+        const auto settle = [&](f32x16_v &x, float top, int sub, int js, const uint64_t (&here2)[kWatch]) {
             // (kept above 0, so that the weight of a score of -inf, a key not attended to, is 0)
-            const float qk = fmaxf(kExact ? qs : ldexpf(qs, -k_exp), 0x1p-126f);
+            const float qk = fmaxf(qs, 0x1p-126f);
             const uint32_t here = (uint32_t)(here2[sub / 2] >> (32 * (sub & 1)));
             const bool whole = js >= all_lo && js + 32 <= all_hi && here == ~0u;
             scale = qk;
@@ -575,7 +568,7 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void k_kvq_chunk(KvqAttnArgs a) {
                 l *= f_grow;
             }
         };
-        // fp16 outputs: the key scales, applied to the scores in fp32
+        // the key scales, applied to the scores in fp32
         const auto scale_keys = [&](f32x16_v &x, int buf, int sub, int i) {
             const float4 f = *reinterpret_cast<const float4 *>(&s_ks[buf][32 * sub + 2 * i + 4 * half]);
             x[i] *= f.x; x[i + 1] *= f.y; x[i + 2] *= f.z; x[i + 3] *= f.w;
@@ -595,7 +588,6 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void k_kvq_chunk(KvqAttnArgs a) {
                 expand_begin(t ? second : stage, from + t * kTile);
 #pragma unroll
                 for (int x = 0; x < kPieces; ++x) expand_piece(t ? second : stage, t, x);
-                k_exps[t] = k_exp_next;
                 v_exps[t] = v_exp_next;
 #pragma unroll
                 for (int i = 0; i < kWatch; ++i) theres[t][i] = there_next[i];
@@ -610,14 +602,12 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void k_kvq_chunk(KvqAttnArgs a) {
                 clear(acc[0]);
 #pragma unroll
                 for (int x = 0; x < kSteps; ++x) mul_k(acc[0], x, read_k(0, 0, x));
-                if (kExact) {
 #pragma unroll
-                    for (int i = 0; i < 16; i += 4) scale_keys(acc[0], 0, 0, i);
-                }
+                for (int i = 0; i < 16; i += 4) scale_keys(acc[0], 0, 0, i);
                 float top = acc[0][0];
 #pragma unroll
                 for (int i = 0; i < 16; i += 2) top = max3(top, acc[0][i], acc[0][i + 1]);
-                settle(acc[0], top, 0, 0, from, k_exps[0], theres[0]);
+                settle(acc[0], top, 0, from, theres[0]);
             }
         }
         const auto load_next = [&](int j) {
@@ -664,7 +654,6 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void k_kvq_chunk(KvqAttnArgs a) {
                 read_first<kN>(ahead, read);
                 if (sub == 0) {
                     expand_begin(stage, j + 2 * kTile);
-                    k_exps[2] = k_exp_next;
                     v_exps[2] = v_exp_next;
                 }
                 f32x16_v &x = acc[cur], &y = acc[nxt];
@@ -694,7 +683,7 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void k_kvq_chunk(KvqAttnArgs a) {
                 };
                 float top = kUnseen;
                 const auto largest = [&](int i) {  // of four of the next scores
-                    if (kExact) scale_keys(y, kb, ks, i);
+                    scale_keys(y, kb, ks, i);
                     top = max3(max3(top, y[i], y[i + 1]), y[i + 2], y[i + 3]);
                 };
                 constexpr int kFirst = kPieces + 1;  // pieces of a tile's first step more than of the others
@@ -730,8 +719,6 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void k_kvq_chunk(KvqAttnArgs a) {
                     v_exp = v_exps[0];
                 }
                 if (wrap) {
-                    k_exps[0] = k_exps[1];
-                    k_exps[1] = k_exps[2];
                     v_exps[0] = v_exps[1];
                     v_exps[1] = v_exps[2];
 #pragma unroll
@@ -741,7 +728,7 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void k_kvq_chunk(KvqAttnArgs a) {
                     }
                 }
                 grow = false;
-                if (!wrap || it + 1 < count) settle(y, top, kb, ks, wrap ? j + kTile : j + 32 * (sub + 1), k_exps[0], theres[0]);
+                if (!wrap || it + 1 < count) settle(y, top, ks, wrap ? j + kTile : j + 32 * (sub + 1), theres[0]);
                 if (kSubs == 1) {
                     x = y;
 #pragma unroll
@@ -761,7 +748,7 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void k_kvq_chunk(KvqAttnArgs a) {
 #pragma unroll
         for (int u = 0; u < kMTiles; ++u)
 #pragma unroll
-            for (int i = 0; i < 16; ++i) o[u][i] = ldexpf(o[u][i] * inv, kOperandShift - v_exp);
+            for (int i = 0; i < 16; ++i) o[u][i] = ldexpf(o[u][i] * inv, kValShift - v_exp);
         if (alone) {
             if (live) {
                 using O = ChunkOut<D>;

@@ -480,8 +480,8 @@ onebit_status_t kvq_dequantize(const kvq_cache_t *cache, const int64_t *slots, i
  * and lse = -inf.  Sums, maxima and lse are binary32.  Roundings before them: of the
  * weights exp(s_j - max) to fp16 (11 bits, ties to even) for bf16 outputs, to two fp16
  * parts for fp16 ones; and, for bf16 and sequences with more than 48 query rows of a
- * cache head (tokens * q_heads / kv_heads), of the keys and values to fp16 (their scale
- * and their product with it, an eighth of an 8-bit code's own step or less).  Weights
+ * cache head (tokens * q_heads / kv_heads), of the values to fp16 (their scale and their
+ * product with it, an eighth of an 8-bit code's own step or less).  Weights
  * and values that far below the largest of their tiles fall out of fp16's range are
  * lost (2^-31 of the largest weight, 2^-14 of the largest scale at most).  A scale that
  * is not finite leaves nothing finite in out (nor, maybe, in lse) for the queries that

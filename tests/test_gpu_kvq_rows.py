@@ -85,3 +85,44 @@ def rows_keep_their_bits(q_len, kv, dtype, bits, dim, junk, window, pages=0):
 def test_drafts_know_nothing_of_later_tokens(dtype, bits, dim, q_len, kv, pages, junk, window):
     """Blocks of 16 rows (tokens x 2), and of 32 under a block table for long caches."""
     rows_keep_their_bits(q_len, kv, dtype, bits, dim, junk, window, pages)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("bits,dim", [(8, 128), (4, 64), (8, 256), (4, 128)])
+@pytest.mark.parametrize("q_len,kv", [(60, 400), (300, 300)])
+@pytest.mark.parametrize("size", [3.0, 30.0, 300.0])
+def test_large_scores_of_chunks_are_as_exact_as_binary32(dtype, bits, dim, q_len, kv, size):
+    """Scores of about `size`, all sums of terms of one sign.  What a score may be off by is then a part
+    of itself: the products' sum in binary32, at most a rounding of 2^-24 for each of D terms (taken
+    twice, the matrix cores may cut where others round), the two scales' roundings, and exp2's argument,
+    2^-22 (s + 1).  lse is off by as much and by its sum's roundings; an output by twice as much of
+    A = sum_j softmax_j |v_j| (the weights and their sum), by the weights' rounding to fp16, 2^-11 A, for
+    bf16 by that of the values and their scales, 2^-10 A + 2^-14 of the largest scale, by its sums, and
+    by its own rounding."""
+    g = gen("large", q_len, dim, bits)
+    q, pools, table, lens, _ = make(g, [q_len], [kv], 4, 2, dim, 16, bits, dtype)
+    zero = kvq_ref.LEVELS[bits][1]
+    code = kvq_ref.unpack(pools[0], bits)
+    pools = (kvq_ref.pack(torch.where(code < zero, 2 * zero - code, code), bits), *pools[1:])
+    q = q.abs()
+    pages, offsets = rows_of(pools, table, 0, range(kv))
+    k, v = (kvq_ref.values(pools[i][pages, :, offsets], pools[i + 1][pages, :, offsets], bits) for i in (0, 2))
+    x = q.double().view(q_len, 2, 2, dim)
+    raw = torch.einsum("tghd,jgd->tghj", x, k)
+    scale = size / float(raw.mean())
+    late = (torch.arange(kv) > torch.arange(kv - q_len, kv).unsqueeze(1)).view(q_len, 1, 1, kv)
+    s = (scale * raw).masked_fill(late, -math.inf)
+    want_lse = torch.logsumexp(s, -1)
+    p = torch.softmax(s, -1)
+    want, a = (torch.einsum("tghj,jgd->tghd", p, t) for t in (v, v.abs()))
+    top = s.amax(-1)
+    off = 2 * (dim + 8) * 2.0 ** -24 * top + 2.0 ** -22 * (top + 1)
+    sums = 2.0 ** -24 * (kv + 64)
+    v_top = float(pools[3][pages, :, offsets].abs().max())
+    tol = a * (2 * off.unsqueeze(-1) + 2.0 ** -11 + 4 * sums) + 2.0 ** -20 * v_top
+    if dtype == BF16:
+        tol = tol + 2.0 ** -10 * a + 2.0 ** -14 * v_top
+    tol = tol + kvq_ref.HALF_STEP[dtype] * (want.abs() + tol)
+    got, lse = attend(q, pools, table, lens, bits, scale=scale)
+    assert ((lse.double().view_as(want_lse) - want_lse).abs() <= off + sums + 2.0 ** -22 * (want_lse.abs() + 1)).all()
+    assert ((got.double().view_as(want) - want).abs() <= tol).all()
