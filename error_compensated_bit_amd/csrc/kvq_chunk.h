@@ -33,6 +33,13 @@
 namespace onebit {
 
 constexpr float kUnseen = -3.40282347e+38f;  // running maximum before the first key
+// Keys enter the products as (c - z) 2^-kKeyShift and their scales are held times
+// 2^-kKeyScaleShift, so that a sum of 256 products (below 2^16) times any scale (below 2^122) stays
+// below 2^127; the query row's factor makes up for both.  (That factor goes below fp32's
+// smallest normal number only where max |q| * |sm_scale| is below 2^-138 and no score is above 1.)
+constexpr int kKeyShift = 14, kKeyScaleShift = 12;
+template <int BITS>
+constexpr float kKeyUnit = (float)(1 << (kCodeShift<BITS> - kKeyShift));
 constexpr int kChunkSeqs = 512;        // sequences of one launch
 constexpr int kChunkMaxGroups = 1024;  // workgroups of one launch
 
@@ -315,7 +322,11 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void k_kvq_chunk(KvqAttnArgs a) {
                                              fabsf(half_bits_to_float<GT>(w[k] >> 16))));
             }
             const int kq = query_exponent(fmaxf(amax, __shfl_xor(amax, 32, 64)));
-            const float up = __uint_as_float(__float_as_uint(pow2(kq)) ^ a.q_sign);
+            qs = ldexpf(a.scale2, kKeyShift + kKeyScaleShift - kq);
+            // A factor of 0 goes into the queries: times the -inf of a key not attended to it would be NaN.
+            const float up = qs == 0.0f ? 0.0f : __uint_as_float(__float_as_uint(pow2(kq)) ^ a.q_sign);
+            qs = qs == 0.0f ? 1.0f : qs;
+            if (a.cap2 > 0.0f) qs *= a.cap_scale;
 #pragma unroll
             for (int s = 0; s < kSteps; ++s) {
                 const uint32_t w[4] = {raw[s].x, raw[s].y, raw[s].z, raw[s].w};
@@ -327,8 +338,6 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void k_kvq_chunk(KvqAttnArgs a) {
                 }
                 qf[s] = query_operand<BITS>(f, up);
             }
-            qs = ldexpf(a.scale2, kUnitShift - kq);
-            if (a.cap2 > 0.0f) qs *= a.cap_scale;
         };
 
         // ---- the tiles' way from the cache into LDS
@@ -468,12 +477,12 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void k_kvq_chunk(KvqAttnArgs a) {
         const auto expand_piece = [&](const Stage &s, int buf, int piece) {
             if (piece < kWide) {
                 uint4 x[2];
-                expand16<BITS>(s.kw[piece], splat16(kUnitScale<BITS>), splat16(-kUnitOffset<BITS>), x);
+                expand16<BITS>(s.kw[piece], splat16(kKeyUnit<BITS>), splat16(-0x1p-17f * kKeyUnit<BITS>), x);
                 uint4 *dst = reinterpret_cast<uint4 *>(&s_k[buf][first_token + k_token][k_dim + 16 * piece]);
                 dst[0] = x[0];
                 dst[1] = x[1];
                 if (k_dim == 0 && piece == 0) {
-                    s_ks[buf][first_token + k_token] = x_ks;
+                    s_ks[buf][first_token + k_token] = x_ks * pow2(-kKeyScaleShift);
                     if (kExact) s_vs[buf][first_token + k_token] = x_kv * vf;
                 }
             } else {
@@ -531,20 +540,17 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void k_kvq_chunk(KvqAttnArgs a) {
         // scores of step `sub` of a tile, whose first token is js: scale, cap and mask, and the
         // running maximum.  `top` is the row's largest raw score where that is all there is to do.
         const auto settle = [&](f32x16_v &x, float top, int sub, int js, const uint64_t (&here2)[kWatch]) {
-            // (kept above 0, so that the weight of a score of -inf, a key not attended to, is 0)
-            const float qk = fmaxf(qs, 0x1p-126f);
             const uint32_t here = (uint32_t)(here2[sub / 2] >> (32 * (sub & 1)));
             const bool whole = js >= all_lo && js + 32 <= all_hi && here == ~0u;
-            scale = qk;
+            scale = qs;
             if (a.cap2 > 0.0f || !whole) {
-                if (a.cap2 > 0.0f) {
-                    if (a.cap2 > kWideCap2) {
+                if (a.cap2 > kWideCap2) {
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) x[i] = capped_wide(x[i] * qk, a.cap2);
-                    } else {
+                    for (int i = 0; i < 16; ++i) x[i] = capped_wide(x[i] * qs, a.cap2);
+                    scale = 1.0f;
+                } else if (a.cap2 > 0.0f) {
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) x[i] = capped(x[i] * qk, a.cap2);
-                    }
+                    for (int i = 0; i < 16; ++i) x[i] = capped(x[i] * qs, a.cap2);
                     scale = 1.0f;
                 }
                 if (!whole) {

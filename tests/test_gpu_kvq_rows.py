@@ -126,3 +126,21 @@ def test_large_scores_of_chunks_are_as_exact_as_binary32(dtype, bits, dim, q_len
     got, lse = attend(q, pools, table, lens, bits, scale=scale)
     assert ((lse.double().view_as(want_lse) - want_lse).abs() <= off + sums + 2.0 ** -22 * (want_lse.abs() + 1)).all()
     assert ((got.double().view_as(want) - want).abs() <= tol).all()
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("q_len", [5, 70])
+@pytest.mark.parametrize("key_exp,scale_exp", [(118, -121), (118, -110), (118, None), (-110, 64), (100, None), (90, -100)])
+@pytest.mark.parametrize("window", [0, 30])
+def test_keys_of_any_size_with_a_scale_that_brings_the_scores_back(dtype, bits, q_len, key_exp, scale_exp, window):
+    """Keys near binary32's ends, and a scale of the scores of 0 (None)."""
+    g = gen("keys", q_len, bits)
+    q, pools, table, lens, offs = make(g, [q_len] * 2, [200, 300], 4, 2, 256, 16, bits, dtype, peaked=0.5)
+    pools[1].mul_(2.0 ** key_exp)
+    scale = 0.0 if scale_exp is None else 2.0 ** scale_exp
+    if scale_exp is not None:       # queries that make the scores of some size
+        q = (q.double() * 2.0 ** max(-8, min(8, -key_exp - scale_exp))).to(dtype)
+    got, lse = attend(q, pools, table, lens, bits, q_offsets=offs, scale=scale, window=window)
+    ref = kvq_ref.attention(q, pools, table, lens, bits=bits, scale=scale, q_offsets=offs, window=window)
+    check(got, lse, ref, dtype)
