@@ -13,9 +13,10 @@
 // the scores in fp32: a scale rounded to fp16 moves all of a token's score by up to one part in
 // 2^11, a quarter of a weight where scores are around 500, and saves nothing (2048 tokens over
 // 32768, bf16: heads of 128 1234 us so, 1223 exact; 64 399 : 409; 256 440 : 444).  Values likewise
-// for fp16 outputs.  For bf16 they are expanded to (c - z) scale 2^k, rounded to fp16: one step in
-// 2^11 of a value, where a code of 8 bits is one in 2^8 of the row's largest and the output
-// one in 2^8.  (Exact they would cost heads of 64 another 14%, of 128 10%, of 256 6%.)
+// for fp16 outputs and where not every row of a workgroup attends to all of a tile.  Elsewhere, for
+// bf16, they are expanded to (c - z) scale 2^k, rounded to fp16: one step in 2^11 of a value, where
+// a code of 8 bits is one in 2^8 of the row's largest and the output one in 2^8.  (Exact throughout
+// they would cost heads of 64 another 14%, of 128 10%, of 256 6%.)
 //
 // The work is one line of tiles, shared out as in the step kernel.  A second kernel
 // joins the partial results: a workgroup's has up to 133 KB, too much for the last
@@ -61,7 +62,6 @@ struct ChunkPartial {
 
 template <int GT, int D, int BITS, int NW>
 struct ChunkShape {
-    static constexpr bool kExact = GT == kGradF16;
     static constexpr int kThreads = 64 * NW, kRows = 32 * NW;
     static constexpr int kTile = D == 256 ? 32 : D == 128 ? 64 : 128;  // tokens
     // A thread expands 16 kWide key dimensions of a token and 4 kWide value dimensions of four.
@@ -120,13 +120,6 @@ __device__ __forceinline__ void expand16(const uint32_t (&w)[BITS / 2], f16x2_v 
         out[k] = make_uint4(fma16(c.x, scale, offset), fma16(c.y, scale, offset), fma16(c.z, scale, offset),
                             fma16(c.w, scale, offset));
     }
-}
-
-// The exponent by which scales up to `top` are taken so that they use fp16's range
-template <int BITS>
-__device__ __forceinline__ int scale_exponent(float top) {
-    const int e = (int)((__float_as_uint(top) >> 23) & 255u) - 126;  // top < 2^e
-    return min(max((BITS == 8 ? 15 : 11) - e, -126), 126);
 }
 
 // Tiles of row tile `rt` of a sequence; base: the first tile's first token.
@@ -191,12 +184,17 @@ __device__ __forceinline__ float lse_of(float m, float l) {
 template <int GT, int D, int BITS, int NW>
 __global__ __launch_bounds__(64 * NW, NW / 4) void k_kvq_chunk(KvqAttnArgs a) {
     using S = ChunkShape<GT, D, BITS, NW>;
-    constexpr bool kExact = S::kExact;
+    constexpr bool kTwo = kTwoPart<GT>;  // weights in two parts, values exact; else scales fold into the values where they can
     constexpr int kTile = S::kTile, kWide = S::kWide, kMTiles = D / 32, kSteps = D / 16;
-    constexpr int kValShift = kExact ? kUnitShift : kCodeShift<BITS>;  // an operand of values is 2^-that of what it stands for
+    // Where a weight by itself goes into the products (values folded), it is taken times 2^kWeightShift to
+    // use fp16's range, and folded scales times 2^kFoldShift more than the row's exponent, so that both ways
+    // add up to outputs in the same units.
+    constexpr int kWeightShift = kTwo ? 0 : 7, kFoldShift = kCodeShift<BITS> - kUnitShift - kWeightShift;
+    constexpr int kTopExp = 118;     // largest exponent of a row's values: 2^(kTopExp + kFoldShift) is a number
+    constexpr int kByRow = 1 << 20;  // in place of a tile's exponent: each row has its own
     __shared__ _Float16 s_k[4][kTile][S::kKeyRow];
     __shared__ _Float16 s_v[4][D][S::kValRow];
-    __shared__ float s_ks[4][kTile], s_vs[4][kExact ? kTile : 1];
+    __shared__ float s_ks[4][kTile], s_vs[4][kTwo ? kTile : 1], s_log[4][kTile];
     __shared__ int64_t s_pre[kChunkSeqs + 1];
     __shared__ int64_t s_scan[NW];
     const int tid = threadIdx.x, lane = tid & 63, wave = uniform((int)(tid >> 6));
@@ -287,7 +285,8 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void k_kvq_chunk(KvqAttnArgs a) {
         const int u1 = uniform((int)udiv((seg_end - item_begin) * tiles, allotted));
         const int r0 = rt * S::kRows, r1 = min(seq.len * a.group, r0 + S::kRows);
         const int t0 = r0 / a.group, t1 = (r1 - 1) / a.group;
-        const int some_lo = kvq_lo(a, seq, t0), some_hi = kvq_hi(seq, t1);  // attended to by some row of the tile
+        const int some_hi = kvq_hi(seq, t1);                                  // attended to by some row of the tile
+        const int every_lo = kvq_lo(a, seq, t1), every_hi = kvq_hi(seq, t0);  // ... by every row
         // (an item that attends to nothing reads nothing: the cache may have no pages)
         const int from = base + u0 * kTile, count = some_hi > base ? u1 - u0 : 0;
         const bool alone = pos == item_begin && seg_end == item_end;
@@ -297,10 +296,8 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void k_kvq_chunk(KvqAttnArgs a) {
         const bool live = r < r1;
         const int my_t = live ? r / a.group : t1;
         const int my_lo = kvq_lo(a, seq, my_t), my_hi = kvq_hi(seq, my_t);
-        // positions that all of the wave's rows attend to; a wave without rows only expands
-        const bool wave_live = r0 + 32 * wave < r1;
-        const int wt0 = (r0 + 32 * wave) / a.group, wt1 = (min(r1, r0 + 32 * wave + 32) - 1) / a.group;
-        const int all_lo = wave_live ? kvq_lo(a, seq, wt1) : 0, all_hi = wave_live ? kvq_hi(seq, wt0) : 0;
+        const bool wave_live = r0 + 32 * wave < r1;  // (a wave without rows only expands)
+        const int wt1 = (min(r1, r0 + 32 * wave + 32) - 1) / a.group;
         f16x8_v qf[kSteps];
         float qs;
         uint4 raw[kSteps];
@@ -370,8 +367,8 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void k_kvq_chunk(KvqAttnArgs a) {
             float ks, kv;  // both scales of the key row
             float4 vs;
             int page;
-            float w_ks[kWatch], w_vs[kWatch];
-            bool w_ok[kWatch], w_there[kWatch];
+            float w_vs[kWatch];
+            bool w_there[kWatch];
         };
         uint64_t there_next[kWatch];  // tokens whose pages are in the cache
         const auto watch_token = [&](int i) { return (64 * i + lane) % kTile; };
@@ -419,10 +416,8 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void k_kvq_chunk(KvqAttnArgs a) {
             for (int i = 0; i < kWatch; ++i) {
                 const int at = j + watch_token(i);
                 const int64_t wr = row_of(p.watch[i], at);
-                s.w_ks[i] = a.c.scales[0][wr];
                 s.w_vs[i] = a.c.scales[1][wr];
                 s.w_there[i] = there_is(p.watch[i]);
-                s.w_ok[i] = s.w_there[i] & (at >= some_lo) & (at < some_hi);
             }
         };
         Pages pages, pages0, pages1;
@@ -431,45 +426,49 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void k_kvq_chunk(KvqAttnArgs a) {
             load_pages(pages0, from);
             load_pages(pages1, from + kTile);
         }
-        // exponent of the value scales of the tile being expanded
-        float v_top = 0.0f;
-        int v_exp_next = 126;
-        float x_ks, x_kv, x_s4[4], vf;  // scales of the tile being expanded, and the values' power of two
-        const auto expand_begin = [&](const Stage &s, int j) {
+        // Value scales are brought into fp16's range by a power of two, chosen for the largest that a
+        // row attends to, itself: other rows' tokens must not decide what is lost of its values.  Where
+        // every row attends to all of a tile the largest is common to them, and its exponent is the
+        // tile's; elsewhere (the diagonal, the front of a window) scales go to the weights in fp32, by their
+        // logarithms in s_log.
+        float v_top = 0.0f;                       // the largest of the former tiles so far
+        int v_exp_top = kTopExp, v_exp_next = 0;  // its exponent; that of the tile being expanded
+        float x_ks, x_vs, x_s4[4];                // what becomes of its scales
+        const auto expand_begin = [&](const Stage &s, int buf, int j) {
+            const bool every = j >= every_lo && j + kTile <= every_hi;
             float vt = 0.0f;
-            bool plain = true;  // every token is attended to by some row and has finite scales
+            bool plain = every;
 #pragma unroll
             for (int i = 0; i < kWatch; ++i) {
-                const float x = fabsf(s.w_ks[i]), y = fabsf(s.w_vs[i]);
-                const bool in = s.w_ok[i] && x < INFINITY && y < INFINITY;
+                const float y = fabsf(s.w_vs[i]);
+                const bool in = s.w_there[i] && y < INFINITY;
                 there_next[i] = __ballot(s.w_there[i]);
                 plain = plain && __ballot(in) == ~0ull;
                 vt = fmaxf(vt, in ? y : 0.0f);
             }
-            if (__any(vt > v_top)) {
+            if (__builtin_expect(every && __any(vt > v_top), 0)) {
 #pragma unroll
                 for (int d = 32; d >= 1; d >>= 1) vt = fmaxf(vt, __shfl_xor(vt, d, 64));
                 v_top = fmaxf(v_top, vt);
-                v_exp_next = uniform(kExact ? value_exponent(v_top) : scale_exponent<BITS>(v_top));
+                v_exp_top = uniform(min(value_exponent(v_top), kTopExp));
             }
-            vf = pow2(v_exp_next);
-            x_ks = s.ks;
-            x_kv = s.kv;
-            x_s4[0] = s.vs.x; x_s4[1] = s.vs.y; x_s4[2] = s.vs.z; x_s4[3] = s.vs.w;
-            if (!plain) {
-                // a scale that is not finite makes the scores of its token NaN and its values 0: NaN
-                // for the rows that attend to it, nothing for the others
-                const bool ok = there_is(s.page);
-                const int at = j + first_token + k_token;
-                const bool in = ok && at >= some_lo && at < some_hi;
-                const bool finite = fabsf(x_ks) < INFINITY && fabsf(x_kv) < INFINITY;
-                x_ks = in ? (finite ? x_ks : NAN) : 0.0f;
-                x_kv = in && finite ? x_kv : 0.0f;
+            v_exp_next = every ? v_exp_top : kByRow;
+            const float vf = pow2(v_exp_top + (kTwo ? 0 : kFoldShift)), v4[4] = {s.vs.x, s.vs.y, s.vs.z, s.vs.w};
+            x_ks = fmaf(s.ks, 0.0f, s.ks) * pow2(-kKeyScaleShift);  // (NaN for an infinite scale)
+            x_vs = s.kv * vf;
 #pragma unroll
-                for (int t = 0; t < 4; ++t) {
-                    const int vat = j + first_token + v_token + t;
-                    x_s4[t] = ok && vat >= some_lo && vat < some_hi && fabsf(x_s4[t]) < INFINITY ? x_s4[t] : 0.0f;
-                }
+            for (int t = 0; t < 4; ++t) x_s4[t] = v4[t] * vf;
+            if (__builtin_expect(!plain, 0)) {
+                // A scale that is not finite makes the scores of its token NaN and its values 0: NaN for the
+                // rows that attend to it, nothing for the others.
+                const bool ok = there_is(s.page), finite = fabsf(s.kv) < INFINITY;
+                x_ks = finite ? x_ks : NAN;
+                x_vs = !every ? copysignf(1.0f, s.kv) : ok && finite ? x_vs : 0.0f;
+#pragma unroll
+                for (int t = 0; t < 4; ++t)
+                    x_s4[t] = !every ? copysignf(kUnitScale<BITS>, v4[t]) : ok && fabsf(v4[t]) < INFINITY ? x_s4[t] : 0.0f;
+                if (!every && k_dim == 0)
+                    s_log[buf][first_token + k_token] = ok && finite ? log2f(fabsf(s.kv)) : -INFINITY;
             }
         };
         // the expansion in pieces: 16 key dimensions, then a dimension of the values at a time
@@ -482,14 +481,14 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void k_kvq_chunk(KvqAttnArgs a) {
                 dst[0] = x[0];
                 dst[1] = x[1];
                 if (k_dim == 0 && piece == 0) {
-                    s_ks[buf][first_token + k_token] = x_ks * pow2(-kKeyScaleShift);
-                    if (kExact) s_vs[buf][first_token + k_token] = x_kv * vf;
+                    s_ks[buf][first_token + k_token] = x_ks;
+                    if (kTwo) s_vs[buf][first_token + k_token] = x_vs;
                 }
             } else {
                 const int d = piece - kWide, w = BITS == 8 ? d / 4 : 0;
                 f16x2_v s2[2];
 #pragma unroll
-                for (int t = 0; t < 4; ++t) s2[t >> 1][t & 1] = (_Float16)(kExact ? kUnitScale<BITS> : x_s4[t] * vf);
+                for (int t = 0; t < 4; ++t) s2[t >> 1][t & 1] = (_Float16)(kTwo ? kUnitScale<BITS> : x_s4[t]);
                 // four tokens are eight bytes; of each 16 tokens, those that one half of a wave
                 // multiplies lie together
                 const int quad = (first_token + v_token) / 4;
@@ -504,9 +503,10 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void k_kvq_chunk(KvqAttnArgs a) {
         f32x16_v o[kMTiles], acc[2];  // outputs; scores of this step and the next
         u32x4_v pw[2][2], lw[2][2];   // weights of this step and the last, each for two products of 16 tokens
         float m = kUnseen, l = 0.0f;
-        float f_grow = 1.0f, scale = 0.0f;
-        bool grow = false;
-        int v_exp = 126;                       // of what the outputs have summed
+        float f_grow = 1.0f, scale = 0.0f, shift = 0.0f, l_keep = 0.0f;
+        bool grow = false, by_row = false;
+        int v_exp = kTopExp;                   // the row's: of what its outputs have summed
+        int l_exp = 0;                         // l is 2^(l_exp + kWeightShift) times the sum of the weights
         int v_exps[3];                         // of tiles it, it + 1, it + 2
         uint64_t theres[2][kWatch];            // of tiles it, it + 1
 #pragma unroll
@@ -530,20 +530,24 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void k_kvq_chunk(KvqAttnArgs a) {
         const auto mul_v = [&](int w, int x, f16x8_v f) {
             const int u = x % kMTiles, t = x / kMTiles;
             o[u] = __builtin_amdgcn_mfma_f32_32x32x16_f16(f, __builtin_bit_cast(f16x8_v, pw[w][t]), o[u], 0, 0, 0);
-            if (kExact)
+            if (kTwo)
                 o[u] = __builtin_amdgcn_mfma_f32_32x32x16_f16(f, __builtin_bit_cast(f16x8_v, lw[w][t]), o[u], 0, 0, 0);
         };
         const auto clear = [](f32x16_v &x) {
 #pragma unroll
             for (int i = 0; i < 16; ++i) x[i] = 0.0f;
         };
-        // scores of step `sub` of a tile, whose first token is js: scale, cap and mask, and the
-        // running maximum.  `top` is the row's largest raw score where that is all there is to do.
-        const auto settle = [&](f32x16_v &x, float top, int sub, int js, const uint64_t (&here2)[kWatch]) {
+        // scores of step `sub` of the tile in `buf`, whose first token is js: scale, cap and mask, and the
+        // row's running maximum and exponent.  `top` is the row's largest raw score where that is all
+        // there is to do; `other`: the tile's exponent is not the last one's.  A row's numbers depend on its
+        // own tokens only.  (Branches are marked as rare where most steps pass them by: laid out in line
+        // they cost 2048 tokens over 32768 8%.)
+        const auto settle = [&](f32x16_v &x, float top, int buf, int sub, int js, int t_exp, bool other, const uint64_t (&here2)[kWatch]) {
             const uint32_t here = (uint32_t)(here2[sub / 2] >> (32 * (sub & 1)));
-            const bool whole = js >= all_lo && js + 32 <= all_hi && here == ~0u;
+            uint32_t mine = ~0u;  // the tokens that this lane's row attends to, one bit each, from its half's first
+            by_row = t_exp == kByRow;
             scale = qs;
-            if (a.cap2 > 0.0f || !whole) {
+            if (__builtin_expect(a.cap2 > 0.0f || by_row || here != ~0u, 0)) {
                 if (a.cap2 > kWideCap2) {
 #pragma unroll
                     for (int i = 0; i < 16; ++i) x[i] = capped_wide(x[i] * qs, a.cap2);
@@ -553,11 +557,10 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void k_kvq_chunk(KvqAttnArgs a) {
                     for (int i = 0; i < 16; ++i) x[i] = capped(x[i] * qs, a.cap2);
                     scale = 1.0f;
                 }
-                if (!whole) {
-                    // the tokens that this lane's row attends to, one bit each, from its half's first
+                if (by_row || here != ~0u) {
                     const int lo = min(max(my_lo - js, 0), 32), hi = min(max(my_hi - js, 0), 32);
                     const uint64_t bits = ((1ull << hi) - 1) & ~((1ull << lo) - 1) & here;
-                    const uint32_t mine = (uint32_t)(bits >> (4 * half));
+                    mine = (uint32_t)(bits >> (4 * half));
 #pragma unroll
                     for (int i = 0; i < 16; ++i)
                         if (!(mine >> (8 * (i / 4) + (i & 3)) & 1)) x[i] = -INFINITY;
@@ -566,12 +569,60 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void k_kvq_chunk(KvqAttnArgs a) {
 #pragma unroll
                 for (int i = 0; i < 16; i += 2) top = max3(top, x[i], x[i + 1]);
             }
-            grow = __any(top * scale > m + 8.0f);
-            if (grow) {
-                top = fmaxf(m, fmaxf(top, __shfl_xor(top, 32, 64)) * scale);
-                f_grow = exp2_fast(m - top);
-                m = top;
-                l *= f_grow;
+            f_grow = 1.0f;
+            grow = false;
+            if (__builtin_expect(other && !by_row, 0)) {
+                // In a tile with an exponent of its own the weights are short of the row's units by the
+                // difference, and l with them.  (2^-90 of a weight is nothing in fp16, while l has room for it.)
+                const int e = min(v_exp, t_exp), le = max(e - t_exp, -90);
+                grow = __any(e != v_exp);
+                f_grow = ldexpf(1.0f, e - v_exp);
+                l = ldexpf(l, le - l_exp);
+                v_exp = e;
+                l_exp = le;
+            }
+            if (__builtin_expect(__any(top * scale > m + 8.0f), 0)) {
+                grow = true;
+                top = fmaxf(top, __shfl_xor(top, 32, 64)) * scale;
+                const bool up = top > m + 8.0f;
+                const float f = up ? exp2_fast(m - top) : 1.0f;
+                m = up ? top : m;
+                l *= f;
+                f_grow *= f;
+            }
+            shift = (float)(kWeightShift + l_exp) - m;
+            if (__builtin_expect(by_row, 0)) {
+                // The logarithms of weight times scale are computed here, with the power of two that brings the
+                // row's largest below 2^15 (they are 2^-18 off), and the weights' sum, so that the loop below
+                // knows nothing of it; it adds up something else for l, which is put right after it.
+                l_keep = l;
+                if (__any(mine != 0)) {
+                    float sum = 0.0f;
+#pragma unroll
+                    for (int i = 0; i < 16; i += 4) {
+                        const float4 v = *reinterpret_cast<const float4 *>(&s_log[buf][32 * sub + 2 * i + 4 * half]);
+                        const float v4[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const float w = fmaf(x[i + k], scale, -m);
+                            sum += exp2_fast(w);
+                            x[i + k] = w + v4[k];
+                        }
+                    }
+                    float most = x[0];
+#pragma unroll
+                    for (int i = 0; i < 16; i += 2) most = max3(most, x[i], x[i + 1]);
+                    most = fmaxf(most, __shfl_xor(most, 32, 64));
+                    const int e = most > -INFINITY ? min(v_exp, 14 - (int)floorf(most)) : v_exp;
+                    grow |= __any(e != v_exp);
+                    f_grow = ldexpf(f_grow, e - v_exp);
+                    v_exp = e;
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) x[i] += (float)e;
+                    l_keep += ldexpf(sum, kWeightShift + l_exp);
+                }
+                scale = 1.0f;
+                shift = 0.0f;
             }
         };
         // the key scales, applied to the scores in fp32
@@ -591,7 +642,7 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void k_kvq_chunk(KvqAttnArgs a) {
             __syncthreads();  // the item before is done with the buffers
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
-                expand_begin(t ? second : stage, from + t * kTile);
+                expand_begin(t ? second : stage, t, from + t * kTile);
 #pragma unroll
                 for (int x = 0; x < kPieces; ++x) expand_piece(t ? second : stage, t, x);
                 v_exps[t] = v_exp_next;
@@ -602,7 +653,6 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void k_kvq_chunk(KvqAttnArgs a) {
                     load_pages(pages, from + 3 * kTile);
                 }
             }
-            v_exp = v_exps[0];
             __syncthreads();
             if (wave_live) {
                 clear(acc[0]);
@@ -613,7 +663,7 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void k_kvq_chunk(KvqAttnArgs a) {
                 float top = acc[0][0];
 #pragma unroll
                 for (int i = 0; i < 16; i += 2) top = max3(top, acc[0][i], acc[0][i + 1]);
-                settle(acc[0], top, 0, from, theres[0]);
+                settle(acc[0], top, 0, 0, from, v_exps[0], true, theres[0]);
             }
         }
         const auto load_next = [&](int j) {
@@ -641,7 +691,7 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void k_kvq_chunk(KvqAttnArgs a) {
                 working = false;
             }
             if (!working) {
-                expand_begin(stage, j + 2 * kTile);
+                expand_begin(stage, fresh, j + 2 * kTile);
 #pragma unroll
                 for (int x = 0; x < kPieces; ++x) expand_piece(stage, fresh, x);
                 load_next(j);
@@ -659,27 +709,25 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void k_kvq_chunk(KvqAttnArgs a) {
                 f16x8_v ahead[kAhead];
                 read_first<kN>(ahead, read);
                 if (sub == 0) {
-                    expand_begin(stage, j + 2 * kTile);
+                    expand_begin(stage, fresh, j + 2 * kTile);
                     v_exps[2] = v_exp_next;
                 }
                 f32x16_v &x = acc[cur], &y = acc[nxt];
                 clear(y);
-                // weights relative to the running maximum, times 2^7: they use fp16's range
-                const float shift = kExact ? -m : 7.0f - m, by = scale;
-                const auto weigh = [&](int q) {  // of two tokens
+                const auto weigh = [&](int q) {  // of two tokens, relative to the running maximum
                     const int i = 2 * q;
                     float e[2];
 #pragma unroll
-                    for (int k = 0; k < 2; ++k) e[k] = exp2_fast(fmaf(x[i + k], by, shift));
+                    for (int k = 0; k < 2; ++k) e[k] = exp2_fast(fmaf(x[i + k], scale, shift));
                     l += e[0] + e[1];
-                    if (kExact) {
+                    if (kTwo) {
                         const float2 v = *reinterpret_cast<const float2 *>(
                             &s_vs[buf][32 * sub + 8 * (i / 4) + 4 * half + (i & 3)]);
                         e[0] *= v.x;
                         e[1] *= v.y;
                     }
                     uint32_t p = round_pair<kGradF16>(e[0], e[1]), rest = 0;
-                    if (kExact) {
+                    if (kTwo) {
                         rest = rest_pair(e[0], e[1], p);
                         pin(rest);
                         lw[cur][i / 8][(i % 8) / 2] = rest;
@@ -709,21 +757,15 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void k_kvq_chunk(KvqAttnArgs a) {
                     weave<kN, kFirst + 12>(ahead, read, product, piece);
                 else
                     weave<kN, 12>(ahead, read, product, piece);
-                // (the last values went in with weights relative to the maximum before this step's,
-                // and with the scales' exponent of their own tile)
-                if (grow) {
+                if (__builtin_expect(by_row, 0)) l = l_keep;
+                // (the last values went in with weights relative to the maximum and the exponent before this step's)
+                if (__builtin_expect(grow, 0)) {
 #pragma unroll
                     for (int u = 0; u < kMTiles; ++u)
 #pragma unroll
                         for (int i = 0; i < 16; ++i) o[u][i] *= f_grow;
                 }
-                if (sub == 0 && v_exp != v_exps[0]) {
-#pragma unroll
-                    for (int u = 0; u < kMTiles; ++u)
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) o[u][i] = ldexpf(o[u][i], v_exps[0] - v_exp);
-                    v_exp = v_exps[0];
-                }
+                const bool other = wrap && v_exps[1] != v_exps[0];
                 if (wrap) {
                     v_exps[0] = v_exps[1];
                     v_exps[1] = v_exps[2];
@@ -734,7 +776,8 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void k_kvq_chunk(KvqAttnArgs a) {
                     }
                 }
                 grow = false;
-                if (!wrap || it + 1 < count) settle(y, top, ks, wrap ? j + kTile : j + 32 * (sub + 1), theres[0]);
+                if (!wrap || it + 1 < count)
+                    settle(y, top, kb, ks, wrap ? j + kTile : j + 32 * (sub + 1), v_exps[0], other, theres[0]);
                 if (kSubs == 1) {
                     x = y;
 #pragma unroll
@@ -750,11 +793,11 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void k_kvq_chunk(KvqAttnArgs a) {
         // ---- results
         l += __shfl_xor(l, 32, 64);
         const float inv = l != 0.0f ? 1.0f / l : 0.0f;
-        if (!kExact) l *= 0x1p-7f;
+        l = ldexpf(l, -kWeightShift - l_exp);
 #pragma unroll
         for (int u = 0; u < kMTiles; ++u)
 #pragma unroll
-            for (int i = 0; i < 16; ++i) o[u][i] = ldexpf(o[u][i] * inv, kValShift - v_exp);
+            for (int i = 0; i < 16; ++i) o[u][i] = ldexpf(o[u][i] * inv, kUnitShift + kWeightShift + l_exp - v_exp);
         if (alone) {
             if (live) {
                 using O = ChunkOut<D>;

@@ -481,11 +481,11 @@ onebit_status_t kvq_dequantize(const kvq_cache_t *cache, const int64_t *slots, i
  * weights exp(s_j - max) to fp16 (11 bits, ties to even) for bf16 outputs, to two fp16
  * parts for fp16 ones; and, for bf16 and sequences with more than 48 query rows of a
  * cache head (tokens * q_heads / kv_heads), of the values to fp16 (their scale and their
- * product with it, an eighth of an 8-bit code's own step or less).  Weights
- * and values that far below the largest of their tiles fall out of fp16's range are
- * lost (2^-31 of the largest weight, 2^-14 of the largest scale at most).  A scale that
- * is not finite leaves nothing finite in out (nor, maybe, in lse) for the queries that
- * attend to its row, and makes no difference to the others.
+ * product with it, an eighth of an 8-bit code's own step or less).  Weights and values
+ * so far below the largest that the same query attends to that they fall out of fp16's
+ * range are lost (2^-31 of the largest weight, 2^-14 of the largest scale at most).  A
+ * scale that is not finite leaves nothing finite in out (nor, maybe, in lse) for the
+ * queries that attend to its row, and makes no difference to the others.
  * NULL q_offsets is the form for single tokens and drafts: one launch instead of three.
  * q: bf16 or fp16 (ONEBIT_ERR_UNSUPPORTED otherwise), addressed as k above.  out:
  * [total_q][q_heads][head_dim], contiguous, of q's type.  lse: fp32 [total_q][q_heads],
@@ -494,10 +494,11 @@ onebit_status_t kvq_dequantize(const kvq_cache_t *cache, const int64_t *slots, i
  * which are used.  The library never reads outside the given arrays: a length is taken
  * as 0 if negative and as max_pages * page if larger, a page number outside
  * [0, n_pages) counts as not attended to, offsets are clamped to 0 .. total_q.  What
- * the cache holds in positions that are not attended to has no influence, whatever its
- * bits.  q_heads a multiple of kv_heads; total_q * q_heads and max_pages * page
- * below 2^31 - 2048; sm_scale from -2^64 to 2^64; softcap 0 or from 2^-64 to 2^64.  Scores
- * are formed in binary32: max |q| * |sm_scale| (with a softcap, twice that over it) is to
+ * the cache holds in positions that a query does not attend to, later tokens of its
+ * draft or chunk among them, has no influence on the query's results, whatever its bits.
+ * q_heads a multiple of kv_heads; total_q * q_heads and max_pages * page below
+ * 2^31 - 2048; sm_scale from -2^64 to 2^64; softcap 0 or from 2^-64 to 2^64.  Scores are
+ * formed in binary32: max |q| * |sm_scale| (with a softcap, twice that over it) is to
  * stay below 2^100, else rows may come out NaN.
  * workspace: kvq_attention_workspace_bytes bytes (on the device that is current), 16-byte
  * aligned, zeroed once before its first use (onebit_workspace_init); every completed

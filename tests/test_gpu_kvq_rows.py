@@ -144,3 +144,41 @@ def test_keys_of_any_size_with_a_scale_that_brings_the_scores_back(dtype, bits, 
     got, lse = attend(q, pools, table, lens, bits, q_offsets=offs, scale=scale, window=window)
     ref = kvq_ref.attention(q, pools, table, lens, bits=bits, scale=scale, q_offsets=offs, window=window)
     check(got, lse, ref, dtype)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("bits,dim", [(8, 128), (4, 64), (8, 256)])
+@pytest.mark.parametrize("q_len,kv", [(70, 70), (70, 900), (300, 333)])
+@pytest.mark.parametrize("junk", JUNK)
+@pytest.mark.parametrize("window", [0, 40, 200])
+def test_chunks_know_nothing_of_later_tokens(dtype, bits, dim, q_len, kv, junk, window):
+    rows_keep_their_bits(q_len, kv, dtype, bits, dim, junk, window)
+
+
+def values_without_sign(codes):
+    """Codes (8 bits) of the magnitudes of the values."""
+    return torch.where(codes < 128, (256 - codes.int()).clamp(max=255).to(torch.uint8), codes)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("q_len,kv", [(24, 60), (70, 70), (300, 340)])
+@pytest.mark.parametrize("step", [3.0, 0.25, -0.25, -3.0])
+def test_scales_that_change_along_the_new_tokens(dtype, q_len, kv, step):
+    """Every new token's values are 2^step times the last one's (from 2^-90 to 2^90 where they would go
+    further).  A query's tolerance counts its own tokens: it is computed for the cache that ends with it."""
+    g = gen("change", q_len)
+    q, pools, table, lens, _ = make(g, [q_len], [kv], 4, 2, 128, 16, 8, dtype, spread=False)
+    pages, offsets = rows_of(pools, table, 0, range(kv))
+    size = torch.exp2(((torch.arange(kv) - kv // 2) * step).clamp(-90, 90).round())
+    if dtype == F16:
+        size = size.clamp(2.0 ** -14, 2.0 ** 8)              # (what the output can hold)
+    pools[3][pages, :, offsets] *= size.unsqueeze(1)
+    got, lse = attend(q, pools, table, lens, 8)
+    for t in sorted({0, 1, 7, 8, q_len // 3, q_len // 2, q_len - 2, q_len - 1}):
+        last = torch.tensor([kv - q_len + t + 1], dtype=torch.int32)
+        ref = kvq_ref.attention(q[t:t + 1], pools, table, last, bits=8, scale=128 ** -0.5)
+        own = float(pools[3][pages[:int(last)], :, offsets[:int(last)]].max())
+        size_of = kvq_ref.attention(q[t:t + 1], (*pools[:2], values_without_sign(pools[2]), pools[3]), table, last, bits=8,
+                                    scale=128 ** -0.5)[0]
+        tol = ref[2] + (2.0 ** -10 * size_of + 2.0 ** -14 * own if dtype == BF16 else 0.0)
+        check(got[t:t + 1], lse[t:t + 1], (ref[0], ref[1], tol, ref[3], ref[4]), dtype)
