@@ -69,8 +69,8 @@ __device__ __forceinline__ KvqSeq kvq_seq(const KvqAttnArgs &a, int b) {
 }
 
 // Positions [lo, hi) that query t of the sequence attends to (hi <= lo: none).
-__device__ __forceinline__ int kvq_hi(const KvqSeq &s, int t) { return max(s.kv - s.len + t + 1, 0); }
-__device__ __forceinline__ int kvq_lo(const KvqAttnArgs &a, const KvqSeq &s, int t) {
+__host__ __device__ __forceinline__ int kvq_hi(const KvqSeq &s, int t) { return max(s.kv - s.len + t + 1, 0); }
+__host__ __device__ __forceinline__ int kvq_lo(const KvqAttnArgs &a, const KvqSeq &s, int t) {
     const int p = s.kv - s.len + t;
     return a.window > 0 && p >= a.window ? p - a.window + 1 : 0;
 }
