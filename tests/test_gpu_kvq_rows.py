@@ -53,14 +53,14 @@ def spoil(pools, table, b, positions, junk, g):
     return tuple(out)
 
 
-def rows_keep_their_bits(q_len, kv, dtype, bits, dim, junk, window, pages=0):
+def rows_keep_their_bits(q_len, kv, dtype, bits, dim, junk, window, pages=0, softcap=0.0, group=2):
     """Tokens of the new ones from the middle on, then those in front of the last queries' windows, hold
-    other values: queries that do not attend to them keep their bits, and the others are right."""
+    other values: queries that do not attend to them keep their bits."""
     g = gen("later", q_len, kv, dim, bits)
-    q, pools, table, lens, _ = make(g, [q_len, q_len], [kv, kv + 37], 4, 2, dim, 16, bits, dtype)
+    q, pools, table, lens, _ = make(g, [q_len, q_len], [kv, kv + 37], 2 * group, 2, dim, 16, bits, dtype)
     if pages > table.shape[1]:
         table = torch.cat((table, torch.full((2, pages - table.shape[1]), -1, dtype=torch.int32)), 1)
-    kw = dict(window=window)
+    kw = dict(window=window, softcap=softcap)
     want, want_lse = attend(q, pools, table, lens, bits, **kw)
     for b in range(2):
         n = int(lens[b])
@@ -153,6 +153,20 @@ def test_keys_of_any_size_with_a_scale_that_brings_the_scores_back(dtype, bits, 
 @pytest.mark.parametrize("window", [0, 40, 200])
 def test_chunks_know_nothing_of_later_tokens(dtype, bits, dim, q_len, kv, junk, window):
     rows_keep_their_bits(q_len, kv, dtype, bits, dim, junk, window)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("q_len,kv", [(24, 300), (70, 333)])
+@pytest.mark.parametrize("softcap", [4.0, 100.0])
+@pytest.mark.parametrize("window", [0, 60])
+@pytest.mark.parametrize("junk", [2.0 ** 100, math.inf])
+def test_later_tokens_under_a_cap(dtype, q_len, kv, softcap, window, junk):
+    rows_keep_their_bits(q_len, kv, dtype, 8, 128, junk, window, softcap=softcap)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+def test_later_tokens_with_more_heads_of_a_cache_head_than_a_tile_has_rows(dtype):
+    rows_keep_their_bits(6, 90, dtype, 8, 64, 2.0 ** 100, 20, group=300)
 
 
 def values_without_sign(codes):
