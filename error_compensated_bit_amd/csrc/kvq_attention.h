@@ -135,7 +135,7 @@ constexpr bool kTwoPart = GT == kGradF16;
 
 __device__ __forceinline__ uint32_t rest_pair(float a, float b, uint32_t pair) {
     const f16x2_v h = __builtin_bit_cast(f16x2_v, pair);
-    // both differences are exact; as fused operations they take the fp16 numbers as they are
+    // both differences are exact (the compiler makes a conversion and a subtraction of each)
     return round_pair<kGradF16>(fmaf((float)h[0], -1.0f, a), fmaf((float)h[1], -1.0f, b));
 }
 

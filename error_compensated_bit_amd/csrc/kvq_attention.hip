@@ -63,15 +63,15 @@ template <int GT, int D, int BITS>
 static void launch(KvqAttnArgs a, hipStream_t s) {
     constexpr int kWide = D == 128 ? 2 : 1, kWaves = chunk_waves(D);
     // Measured with 48 rows against the chunk kernel (us, 8 x 4096 tokens / 32 x 16384, 8 heads):
-    // bf16 heads of 64 25 : 41 / 217 : 291, of 128 39 : 55 / 372 : 428, fp16 39 : 72 / 396 : 607; one
-    // sequence of 16384 38 : 37; with 64 rows and bf16 56 : 55 / 606 : 428.
+    // bf16 heads of 64 25 : 42 / 214 : 298, of 128 38 : 55 / 374 : 444, fp16 39 : 70 / 390 : 587; one
+    // sequence of 16384 38 : 37; with 64 rows and bf16 57 : 55 / 623 : 444.
     a.max_rows = 48;
     const int64_t rows = (int64_t)a.q_uniform * a.group;  // of every sequence, where that is known
     if (a.q_offsets || rows <= a.max_rows) {
         // 17 to 32 rows at once read the cache once, but leave room for fewer workgroups and join more
         // slowly.  That pays with heads of 128, where a second reading would come from memory and not
         // from the 256 MB cache in front of it (as far as the tables tell): 32 rows, 8 heads, 32 x 16384
-        // tokens 266 : 327 us, but 32 x 2000 63 : 57, 8 x 4096 60 : 39, 1 x 16384 102 : 47.  With heads
+        // tokens 270 : 329 us, but 32 x 2000 63 : 58, 8 x 4096 60 : 39, 1 x 16384 102 : 48.  With heads
         // of 64 it is 180 : 181 at the best.
         const int64_t most = a.q_offsets ? a.group : rows;
         const bool wide = kWide == 2 && most > 16 && most <= 32 &&

@@ -13,7 +13,7 @@
 // the scores in fp32: a scale rounded to fp16 moves all of a token's score by up to one part in
 // 2^11, a quarter of a weight where scores are around 500, and saves nothing (2048 tokens over
 // 32768, bf16: heads of 128 1234 us so, 1223 exact; 64 399 : 409; 256 440 : 444).  Values likewise
-// for fp16 outputs and where not every row of a workgroup attends to all of a tile.  Elsewhere, for
+// for fp16 outputs, and where not every row of a workgroup attends to all of a tile.  Elsewhere, for
 // bf16, they are expanded to (c - z) scale 2^k, rounded to fp16: one step in 2^11 of a value, where
 // a code of 8 bits is one in 2^8 of the row's largest and the output one in 2^8.  (Exact throughout
 // they would cost heads of 64 another 14%, of 128 10%, of 256 6%.)
@@ -22,11 +22,11 @@
 // joins the partial results: a workgroup's has up to 133 KB, too much for the last
 // one of an item to read them all.
 //
-// Measured: 2048 new tokens over 32768, 32/8 heads of 128, bf16, 1240 us (0.86 PFLOP/s;
-// a library product of 8192^3 reaches 1.14, a bare loop of these products with their
-// operands from LDS and as many vector operations 1.09); first chunks of 1500 to 4000
-// tokens, 16 heads of 64, fp16, 168 us; 9 chunks of up to 700 tokens, 16/4 heads of 256,
-// 4 bits, cap and window, 244 us, bound by issue with one wave on each SIMD.
+// Measured: 2048 new tokens over 32768, 32/8 heads of 128, bf16, 1230 to 1290 us (0.82 to
+// 0.86 PFLOP/s; a library product of 8192^3 reaches 1.14; the matrix units are busy in 40% of a
+// SIMD's cycles, and other vector instructions take as many again); first chunks of 1500 to
+// 4000 tokens, 16 heads of 64, fp16, 175 us, bf16 140; 9 chunks of up to 700 tokens, 16/4
+// heads of 256, 4 bits, cap and window, 240 us, bound by issue with one wave on each SIMD.
 #pragma once
 
 #include "kvq_attention.h"
@@ -246,7 +246,7 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void k_kvq_chunk(KvqAttnArgs a) {
         __syncthreads();
     }
     const int64_t total = uniform(s_pre[kChunkSeqs]);
-    // A stretch has a tile at least.  (Small calls, against four tiles at least: 64 tokens over 1000 32 -> 25 us
+    // A stretch is allotted a tile at least, of the set-up's or the cache's.  (Small calls, against four tiles at least: 64 tokens over 1000 32 -> 25 us
     // with 8 heads of 64, 34 -> 31 us with heads of 128; the worst of 36 shapes 42 -> 43 us.)
     const int64_t groups = min((int64_t)gridDim.x, udiv(total + 15, 16));
     if (tid == 0) splits[blockIdx.x].last = -1;

@@ -1,5 +1,6 @@
 // kvq_step.h -- attention of few query rows over the coded cache (a token or some
-// drafts for each sequence): bound by reading the cache once.
+// drafts for each sequence): bound by reading the cache, once for 16 query rows of a cache
+// head (or 32, where the caller's tables are for long caches), again for the next.
 //
 // A wave takes 32 tokens at a time straight from memory into the operands' registers,
 // no LDS and no barrier in the loop.  S^T = K Q^T: the lane that holds a query row in
@@ -14,9 +15,9 @@
 // left as a partial result, and the last of its workgroups to arrive joins them, in
 // the order of the line.
 //
-// Measured: 64 sequences of 100 to 16000 tokens, 8 heads of 128, 4 bits, 152 us for
-// 0.67 GB (4.4 TB/s; a copy moves 4.8); 2 of 131072, 8 bits, 126 us (4.4 TB/s); 24 x 5
-// drafts over 900 to 5000, 16 heads of 64, 38 us (4.2 TB/s).  A single sequence of
+// Measured: 64 sequences of 100 to 16000 tokens, 8 heads of 128, 4 bits, 155 us for
+// 0.67 GB (4.3 TB/s; a copy moves 4.8); 2 of 131072, 8 bits, 126 us (4.4 TB/s); 24 x 5
+// drafts over 900 to 5000, 16 heads of 64, 36 us (4.4 TB/s).  A single sequence of
 // 1000 tokens takes 11 us, waits for memory one after the other.
 #pragma once
 
