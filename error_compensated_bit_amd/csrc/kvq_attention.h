@@ -28,6 +28,8 @@ typedef uint32_t u32x4_v __attribute__((ext_vector_type(4)));
 template <int BITS>
 constexpr int kCodeShift = BITS == 8 ? 24 : 20;
 
+constexpr float kNone = -3.40282347e+38f;  // running maximum before the first key
+
 struct KvqAttnArgs {
     KvqCache c;
     const uint16_t *q;
@@ -73,6 +75,12 @@ __host__ __device__ __forceinline__ int kvq_hi(const KvqSeq &s, int t) { return 
 __host__ __device__ __forceinline__ int kvq_lo(const KvqAttnArgs &a, const KvqSeq &s, int t) {
     const int p = s.kv - s.len + t;
     return a.window > 0 && p >= a.window ? p - a.window + 1 : 0;
+}
+
+// Four consecutive outputs, rounded to their type.
+template <int GT>
+__device__ __forceinline__ void store_out4(uint16_t *p, const float (&v)[4]) {
+    *reinterpret_cast<uint2 *>(p) = make_uint2(round_pair<GT>(v[0], v[1]), round_pair<GT>(v[2], v[3]));
 }
 
 // Eight codes of consecutive dimensions as an operand of a product over dimensions.

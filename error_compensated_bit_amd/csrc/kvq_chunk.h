@@ -33,7 +33,6 @@
 
 namespace onebit {
 
-constexpr float kUnseen = -3.40282347e+38f;  // running maximum before the first key
 // Keys enter the products as (c - z) 2^-kKeyShift and their scales are held times
 // 2^-kKeyScaleShift, so that a sum of 256 products (below 2^16) times any scale (below 2^122) stays
 // below 2^127; the query row's factor makes up for both.  (That factor goes below fp32's
@@ -179,10 +178,6 @@ struct ChunkOut {
     }
 };
 
-template <int GT>
-__device__ __forceinline__ void store_four(const KvqAttnArgs &a, int64_t row, int d, int dims, const float (&v)[4]) {
-    *reinterpret_cast<uint2 *>(a.out + row * dims + d) = make_uint2(round_pair<GT>(v[0], v[1]), round_pair<GT>(v[2], v[3]));
-}
 __device__ __forceinline__ int64_t out_row(const KvqAttnArgs &a, int q0, int g, int r) {
     return (int64_t)(q0 + r / a.group) * a.q_heads + g * a.group + r % a.group;
 }
@@ -511,7 +506,7 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void k_kvq_chunk(KvqAttnArgs a) {
         constexpr int kSubs = kTile / 32, kPv = 2 * kMTiles;
         f32x16_v o[kMTiles], acc[2];  // outputs; scores of this step and the next
         u32x4_v pw[2][2], lw[2][2];   // weights of this step and the last, each for two products of 16 tokens
-        float m = kUnseen, l = 0.0f;
+        float m = kNone, l = 0.0f;
         float f_grow = 1.0f, scale = 0.0f, shift = 0.0f, l_keep = 0.0f;
         bool grow = false, by_row = false;
         int v_exp = kTopExp;                   // the row's: of what its outputs have summed
@@ -744,7 +739,7 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void k_kvq_chunk(KvqAttnArgs a) {
                     pin(p);
                     pw[cur][i / 8][(i % 8) / 2] = p;
                 };
-                float top = kUnseen;
+                float top = kNone;
                 const auto largest = [&](int i) {  // of four of the next scores
                     scale_keys(y, kb, ks, i);
                     top = max3(max3(top, y[i], y[i + 1]), y[i + 2], y[i + 3]);
@@ -815,7 +810,7 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void k_kvq_chunk(KvqAttnArgs a) {
                 for (int q = 0; q < O::kQuads; ++q) {
                     const float v[4] = {o[O::u_of(q, 0)][O::i_of(q, 0)], o[O::u_of(q, 1)][O::i_of(q, 1)],
                                         o[O::u_of(q, 2)][O::i_of(q, 2)], o[O::u_of(q, 3)][O::i_of(q, 3)]};
-                    store_four<GT>(a, to, O::dim_of(q, half), D, v);
+                    store_out4<GT>(a.out + to * D + O::dim_of(q, half), v);
                 }
                 if (a.lse && half == 0) a.lse[to] = lse_of(m, l);
             }
@@ -902,7 +897,7 @@ __global__ __launch_bounds__(64 * kJoinWaves) void k_kvq_chunk_join(KvqAttnArgs 
         const int quarter = lines > 1 ? task % lines : line;
         const ChunkSplit s = splits[begin];
         if (32 * wave >= s.rows) continue;
-        float v[kMine][4], m = kUnseen, l = 0.0f;
+        float v[kMine][4], m = kNone, l = 0.0f;
 #pragma unroll
         for (int q = 0; q < kMine; ++q)
 #pragma unroll
@@ -966,7 +961,7 @@ __global__ __launch_bounds__(64 * kJoinWaves) void k_kvq_chunk_join(KvqAttnArgs 
 #pragma unroll
             for (int q = 0; q < kMine; ++q) {
                 const float x[4] = {v[q][0] * inv, v[q][1] * inv, v[q][2] * inv, v[q][3] * inv};
-                store_four<GT>(a, to, O::dim_of(kMine * quarter + q, half), D, x);
+                store_out4<GT>(a.out + to * D + O::dim_of(kMine * quarter + q, half), x);
             }
             if (a.lse && quarter == 0 && half == 0) a.lse[to] = lse_of(m, l);
         }

@@ -32,7 +32,6 @@ constexpr int kStepSeqs = 1024;             // sequences of one launch
 constexpr int kStepMaxGroups = 2048;        // workgroups of one launch
 constexpr int kStepHeader = 4 * kStepMaxGroups;  // bytes of counters in front of the partial results
 constexpr int kJoin = 8;                    // partial results that a join reads at once
-constexpr float kNone = -3.40282347e+38f;   // running maximum before the first key
 
 // A weight may exceed the running maximum's by 2^8 before the sums are rescaled.
 constexpr float kSlack = 8.0f;
@@ -64,11 +63,6 @@ __device__ __forceinline__ float over_quarters_max(float v) {
 __device__ __forceinline__ float over_quarters_sum(float v) {
     v += __shfl_xor(v, 16, 64);
     return v + __shfl_xor(v, 32, 64);
-}
-
-template <int GT>
-__device__ __forceinline__ void store_out4(uint16_t *p, const float (&v)[4]) {
-    *reinterpret_cast<uint2 *>(p) = make_uint2(round_pair<GT>(v[0], v[1]), round_pair<GT>(v[2], v[3]));
 }
 
 template <int D, int BITS>
