@@ -175,24 +175,28 @@ def values_without_sign(codes):
 
 
 @pytest.mark.parametrize("dtype", [BF16, F16])
-@pytest.mark.parametrize("q_len,kv", [(24, 60), (70, 70), (300, 340)])
+@pytest.mark.parametrize("q_len,kv,dim", [(24, 60, 128), (70, 70, 128), (300, 340, 128), (200, 900, 64), (150, 700, 256)])
 @pytest.mark.parametrize("step", [3.0, 0.25, -0.25, -3.0])
-def test_scales_that_change_along_the_new_tokens(dtype, q_len, kv, step):
-    """Every new token's values are 2^step times the last one's (from 2^-90 to 2^90 where they would go
-    further).  A query's tolerance counts its own tokens: it is computed for the cache that ends with it."""
+@pytest.mark.parametrize("window", [0, 300])
+def test_scales_that_change_along_the_tokens(dtype, q_len, kv, dim, step, window):
+    """Every token's values are 2^step times the last one's (from 2^-90 to 2^90 where they would go
+    further).  A query's tolerance counts its own tokens only: it is computed for the cache that ends with
+    it, and for bf16 allows for the values' rounding in chunks, 2^-10 A and 2^-14 of the largest scale."""
     g = gen("change", q_len)
-    q, pools, table, lens, _ = make(g, [q_len], [kv], 4, 2, 128, 16, 8, dtype, spread=False)
+    q, pools, table, lens, _ = make(g, [q_len], [kv], 4, 2, dim, 16, 8, dtype, spread=False)
     pages, offsets = rows_of(pools, table, 0, range(kv))
-    size = torch.exp2(((torch.arange(kv) - kv // 2) * step).clamp(-90, 90).round())
+    size = torch.exp2(((torch.arange(kv) - (kv - q_len // 2)) * step).clamp(-90, 90).round())
     if dtype == F16:
         size = size.clamp(2.0 ** -14, 2.0 ** 8)              # (what the output can hold)
     pools[3][pages, :, offsets] *= size.unsqueeze(1)
-    got, lse = attend(q, pools, table, lens, 8)
+    magnitudes = (*pools[:2], values_without_sign(pools[2]), pools[3])
+    kw = dict(bits=8, scale=dim ** -0.5, window=window)
+    got, lse = attend(q, pools, table, lens, **kw)
     for t in sorted({0, 1, 7, 8, q_len // 3, q_len // 2, q_len - 2, q_len - 1}):
-        last = torch.tensor([kv - q_len + t + 1], dtype=torch.int32)
-        ref = kvq_ref.attention(q[t:t + 1], pools, table, last, bits=8, scale=128 ** -0.5)
-        own = float(pools[3][pages[:int(last)], :, offsets[:int(last)]].max())
-        size_of = kvq_ref.attention(q[t:t + 1], (*pools[:2], values_without_sign(pools[2]), pools[3]), table, last, bits=8,
-                                    scale=128 ** -0.5)[0]
-        tol = ref[2] + (2.0 ** -10 * size_of + 2.0 ** -14 * own if dtype == BF16 else 0.0)
+        n = kv - q_len + t + 1                               # tokens up to the query's own
+        ref = kvq_ref.attention(q[t:t + 1], pools, table, torch.tensor([n]), **kw)
+        first = max(0, n - window) if window else 0
+        own = float(pools[3][pages[first:n], :, offsets[first:n]].max())
+        a = kvq_ref.attention(q[t:t + 1], magnitudes, table, torch.tensor([n]), **kw)[0]
+        tol = ref[2] + (2.0 ** -10 * a + 2.0 ** -14 * own if dtype == BF16 else 0.0)
         check(got[t:t + 1], lse[t:t + 1], (ref[0], ref[1], tol, ref[3], ref[4]), dtype)
