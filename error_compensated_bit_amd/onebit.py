@@ -62,6 +62,11 @@ _SIGS = {
     "qsdp_error_stats": (_I, [_P, _P, _I64, _P, _P, _P, _P]),
     "qsdp_mean_abs_error": (_I, [_P, _P, _I64, _I, _P, _P, _P]),
     "kvq_quantize": (_I, [_P, _P, _I, _I64, _I64, _I64, _I64, _I64, _P, _P, _P]),
+    "qsdp_linear_workspace_bytes": (_SZ, [_I64, _I64, _I64]),
+    "qsdp_linear": (_I, [_P, _I, _I64, _I64, _P, _P, _I64, _P, _SZ, _P]),
+    "qsdp_linear_grad": (_I, [_P, _I, _I64, _I64, _P, _P, _I64, _P, _SZ, _P]),
+    "kvq_append": (_I, [_P, _P, _P, _I, _I64, _I, _I64, _I64, _I64, _I64, _I64, _I64, _P, _P, _I64, _I, _I, _P, _P, _P,
+                        _I64, _I64, _P]),
     "kvq_dequantize": (_I, [_P, _P, _I64, _P, _P, _I, _P]),
     "kvq_attention_workspace_bytes": (_SZ, [_I64, _I64, _I, _I, _I]),
     "kvq_attention": (_I, [_P, _I, _I64, _I, _I64, _I64, _P, _P, _I64, _P, _I64, _I64, _P, _D, _D, _I, _P, _P, _P, _SZ,
@@ -69,6 +74,7 @@ _SIGS = {
 }
 
 QSDP_STATS_PARTIALS = 1024
+QSDP_LINEAR_EXACT_TOKENS = 64
 
 _lib = None
 
@@ -429,12 +435,12 @@ def qsdp_mean_abs_error(x_bf16, ysum, seeds, out, partials, stream=None):
                                       _stream(stream)), "qsdp_mean_abs_error")
 
 
-# ------------------------------------------------ coded key/value cache
+# ------------------------------------------------ products with coded weights
 
-class KvqCache(C.Structure):
-    """kvq_cache_t."""
-    _fields_ = [("k_codes", _P), ("k_scales", _P), ("v_codes", _P), ("v_scales", _P), ("n_pages", _I64),
-                ("page", _I), ("kv_heads", _I), ("head_dim", _I), ("bits", _I)]
+class QsdpMatrix(C.Structure):
+    """qsdp_matrix_t."""
+    _fields_ = [("codes", _P), ("bucket_min", _P), ("bucket_max", _P), ("rows", _I64), ("cols", _I64), ("bucket", _I),
+                ("bits", _I)]
 
 
 def _same_device(first, *tensors) -> int:
@@ -454,6 +460,85 @@ def _dense(t, dtype, what):
     if not t.is_contiguous():
         raise ValueError(f"{what} must be contiguous")
     return t.data_ptr()
+
+
+def _call(name, index, stream, *args):
+    """Run the call with the tensors' device as the current one, on `stream` (default: that
+    device's current stream)."""
+    import torch
+    if stream is None:
+        # the stream's number itself: building a Stream object takes longer than a small call's kernel
+        stream = torch._C._cuda_getCurrentRawStream(index)
+    elif not isinstance(stream, int):
+        if stream.device.index != index:
+            raise ValueError(f"the stream is on {stream.device}, the tensors are on cuda:{index}")
+        stream = stream.cuda_stream
+    call = getattr(_lib or load(), name)
+    if torch.cuda.current_device() == index:
+        status = call(*args, stream)
+    else:
+        with torch.cuda.device(index):
+            status = call(*args, stream)
+    _check(status, name)
+
+
+def _matrix_rows(t, what):
+    """Stride of a [tokens, length] tensor whose rows are dense."""
+    shape, strides = t.shape, t.stride()
+    if len(shape) != 2:
+        raise ValueError(f"{what} must have two dimensions, got {list(shape)}")
+    if strides[1] != 1 and shape[1] > 1:
+        raise ValueError(f"the rows of {what} must be contiguous")
+    # (the stride of a dimension of one entry is never used and may be anything)
+    return strides[0] if shape[0] > 1 else shape[1] + -shape[1] % 8
+
+
+def _linear(name, x, y, rows, cols, codes, bucket_min, bucket_max, bucket, bits, workspace, stream):
+    import torch
+    device = _same_device(x, y, codes, bucket_min, bucket_max, workspace)
+    if x.dtype != y.dtype or x.shape[0] != y.shape[0]:
+        raise ValueError("input and output must have one type and as many rows")
+    if bits not in (4, 8):
+        raise ValueError(f"bits must be 4 or 8, got {bits}")
+    if not 1 <= bucket <= 65536:
+        raise ValueError(f"bucket must be from 1 to 65536, got {bucket}")
+    n = rows * cols
+    buckets = -(-n // bucket)
+    if codes.numel() != (n * bits + 7) // 8 or bucket_min.numel() != buckets or bucket_max.numel() != buckets:
+        raise ValueError(f"{rows} x {cols} weights in buckets of {bucket} need {(n * bits + 7) // 8} bytes of codes and "
+                         f"{buckets} minima and maxima, got {codes.numel()}, {bucket_min.numel()} and {bucket_max.numel()}")
+    if not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    w = QsdpMatrix(_dense(codes, torch.uint8, "codes"), _dense(bucket_min, torch.float32, "bucket_min"),
+                   _dense(bucket_max, torch.float32, "bucket_max"), rows, cols, bucket, bits)
+    _call(name, device, stream, x.data_ptr(), _dtype_code(x), x.shape[0], _matrix_rows(x, "the input"), C.byref(w),
+          y.data_ptr(), _matrix_rows(y, "the output"), workspace.data_ptr(),
+          workspace.numel() * workspace.element_size())
+
+
+def qsdp_linear_workspace_bytes(tokens, rows, cols) -> int:
+    """Bytes for the current device, for qsdp_linear and qsdp_linear_grad; 0 for sizes that they refuse."""
+    return int(load().qsdp_linear_workspace_bytes(int(tokens), int(rows), int(cols)))
+
+
+def qsdp_linear(x, codes, bucket_min, bucket_max, out, *, bucket, bits, workspace, stream=None):
+    """out = x w^T.  x: [tokens, cols], out: [tokens, rows], bf16 or fp16 (any row stride); codes, bucket_min,
+    bucket_max: a [rows, cols] matrix as qsdp_quantize codes it."""
+    _linear("qsdp_linear", x, out, out.shape[-1], x.shape[-1], codes, bucket_min, bucket_max, bucket, bits, workspace, stream)
+
+
+def qsdp_linear_grad(dy, codes, bucket_min, bucket_max, dx, *, bucket, bits, workspace, stream=None):
+    """dx = dy w.  dy: [tokens, rows], dx: [tokens, cols]; the rest as in qsdp_linear."""
+    _linear("qsdp_linear_grad", dy, dx, dy.shape[-1], dx.shape[-1], codes, bucket_min, bucket_max, bucket, bits, workspace,
+            stream)
+
+
+# ------------------------------------------------ coded key/value cache
+
+class KvqCache(C.Structure):
+    """kvq_cache_t."""
+    _fields_ = [("k_codes", _P), ("k_scales", _P), ("v_codes", _P), ("v_scales", _P), ("n_pages", _I64),
+                ("page", _I), ("kv_heads", _I), ("head_dim", _I), ("bits", _I)]
 
 
 def _kvq_cache(k_codes, k_scales, v_codes, v_scales, bits):
@@ -492,26 +577,6 @@ def _kvq_slots(slots, tokens):
     return _dense(slots, torch.int64, "slots")
 
 
-def _kvq_call(name, index, stream, *args):
-    """Run the call with the tensors' device as the current one, on `stream` (default: that
-    device's current stream)."""
-    import torch
-    if stream is None:
-        # the stream's number itself: building a Stream object takes longer than a small call's kernel
-        stream = torch._C._cuda_getCurrentRawStream(index)
-    elif not isinstance(stream, int):
-        if stream.device.index != index:
-            raise ValueError(f"the stream is on {stream.device}, the tensors are on cuda:{index}")
-        stream = stream.cuda_stream
-    call = getattr(_lib or load(), name)
-    if torch.cuda.current_device() == index:
-        status = call(*args, stream)
-    else:
-        with torch.cuda.device(index):
-            status = call(*args, stream)
-    _check(status, name)
-
-
 def kvq_quantize(k, v, slots, k_codes, k_scales, v_codes, v_scales, *, bits, stream=None):
     """k, v: [tokens, kv_heads, head_dim] (any token and head strides); slots: int64 [tokens]."""
     device = _same_device(k, v, slots, k_codes, k_scales, v_codes, v_scales)
@@ -520,8 +585,42 @@ def kvq_quantize(k, v, slots, k_codes, k_scales, v_codes, v_scales, *, bits, str
         raise ValueError("k and v must have one shape and type")
     kt, kh = _kvq_rows(k, cache.kv_heads, cache.head_dim, "k")
     vt, vh = _kvq_rows(v, cache.kv_heads, cache.head_dim, "v")
-    _kvq_call("kvq_quantize", device, stream, k.data_ptr(), v.data_ptr(), _dtype_code(k), k.shape[0], kt, kh, vt, vh,
+    _call("kvq_quantize", device, stream, k.data_ptr(), v.data_ptr(), _dtype_code(k), k.shape[0], kt, kh, vt, vh,
               _kvq_slots(slots, k.shape[0]), C.byref(cache))
+
+
+def kvq_append(q, k, v, positions, rotary, slots, k_codes, k_scales, v_codes, v_scales, q_out, *, bits, interleaved=False,
+               stream=None):
+    """q, q_out: [tokens, q_heads, head_dim] (q_out may be q; both None: keys and values only); k, v: [tokens,
+    kv_heads, head_dim]; any token and head strides, one type; positions, slots: int64 [tokens]; rotary: float32
+    [max_position, rot_dim], cosines and then sines."""
+    import torch
+    device = _same_device(k, v, q, q_out, positions, rotary, slots, k_codes, k_scales, v_codes, v_scales)
+    cache = _kvq_cache(k_codes, k_scales, v_codes, v_scales, bits)
+    if k.dtype != v.dtype or k.shape != v.shape:
+        raise ValueError("k and v must have one shape and type")
+    kt, kh = _kvq_rows(k, cache.kv_heads, cache.head_dim, "k")
+    vt, vh = _kvq_rows(v, cache.kv_heads, cache.head_dim, "v")
+    tokens, heads = k.shape[0], 0
+    qt = qh = ot = oh = 0
+    if (q is None) != (q_out is None):
+        raise ValueError("q and q_out are given both or not at all")
+    if q is not None:
+        if q.dtype != k.dtype or q_out.dtype != k.dtype:
+            raise ValueError("q, q_out and k must have one type")
+        if q.dim() != 3 or q.shape[0] != tokens or q_out.shape != q.shape:
+            raise ValueError(f"q and q_out must both be [{tokens}, q_heads, head_dim]")
+        heads = q.shape[1]
+        qt, qh = _kvq_rows(q, heads, cache.head_dim, "q")
+        ot, oh = _kvq_rows(q_out, heads, cache.head_dim, "q_out")
+    if positions.dim() != 1 or positions.shape[0] != tokens:
+        raise ValueError(f"positions must be [{tokens}], got {list(positions.shape)}")
+    if rotary.dim() != 2:
+        raise ValueError(f"rotary must be [max_position, rot_dim], got {list(rotary.shape)}")
+    _call("kvq_append", device, stream, None if q is None else q.data_ptr(), k.data_ptr(), v.data_ptr(), _dtype_code(k),
+          tokens, heads, qt, qh, kt, kh, vt, vh, _dense(positions, torch.int64, "positions"),
+          _dense(rotary, torch.float32, "rotary"), rotary.shape[0], rotary.shape[1], int(interleaved),
+          _kvq_slots(slots, tokens), C.byref(cache), None if q is None else q_out.data_ptr(), ot, oh)
 
 
 def kvq_dequantize(k_codes, k_scales, v_codes, v_scales, slots, k_out, v_out, *, bits, stream=None):
@@ -531,7 +630,7 @@ def kvq_dequantize(k_codes, k_scales, v_codes, v_scales, slots, k_out, v_out, *,
     if k_out.dtype != v_out.dtype or k_out.shape != v_out.shape:
         raise ValueError("k_out and v_out must have one shape and type")
     _kvq_rows(k_out, cache.kv_heads, cache.head_dim, "k_out")
-    _kvq_call("kvq_dequantize", device, stream, C.byref(cache), _kvq_slots(slots, k_out.shape[0]), k_out.shape[0],
+    _call("kvq_dequantize", device, stream, C.byref(cache), _kvq_slots(slots, k_out.shape[0]), k_out.shape[0],
               _dense(k_out, k_out.dtype, "k_out"), _dense(v_out, v_out.dtype, "v_out"), _dtype_code(k_out))
 
 
@@ -569,7 +668,7 @@ def kvq_attention(q, k_codes, k_scales, v_codes, v_scales, block_table, kv_lens,
         raise ValueError("workspace must be contiguous")
     if abs(window) >= 2 ** 31:                 # (would be cut to 32 bits on its way)
         raise ValueError(f"window must be from 0 to 2^31 - 1, got {window}")
-    _kvq_call("kvq_attention", device, stream, q.data_ptr(), _dtype_code(q), total, q_heads, qt, qh,
+    _call("kvq_attention", device, stream, q.data_ptr(), _dtype_code(q), total, q_heads, qt, qh,
               None if q_offsets is None else _dense(q_offsets, torch.int32, "q_offsets"),
               _dense(kv_lens, torch.int32, "kv_lens"), batch, block_table.data_ptr(), max_pages,
               block_table.stride(0) if batch > 1 else max_pages, C.byref(cache),

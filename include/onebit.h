@@ -1,6 +1,7 @@
 /*
  * onebit.h -- C ABI of the MI355X (gfx950) library for the data-parallel hot path
- * of 1-bit Adam and for a QSDP-style stochastic-rounding quantizer.
+ * of 1-bit Adam, for a QSDP-style stochastic-rounding quantizer and for products with
+ * its codes, and for a key/value cache held in codes.
  *
  * Sources ("the pages"):
  *  [1BA]  nubint.ai review of "1-bit Adam: Communication Efficient Large-Scale
@@ -409,6 +410,55 @@ onebit_status_t qsdp_error_stats(const uint16_t *x_bf16, const float *y, int64_t
 onebit_status_t qsdp_mean_abs_error(const uint16_t *x_bf16, const double *ysum, int64_t n, int seeds,
                                     double *out, double *partials, void *stream);
 
+/* ------------------------------------------------------------------ products with coded weights
+ * A matrix of `rows` x `cols` weights in qsdp_quantize's codes: the flat vector of its rows,
+ * n = rows * cols values, so that weight (o, i) is value o * cols + i of the vector,
+ *   w_{o,i} = min_b + code * delta_b,  b = (o * cols + i) / bucket,
+ * with delta_b as above; buckets may run across rows.
+ *   codes, bucket_min, bucket_max: as qsdp_quantize wrote them for n values.
+ *   cols and bucket are multiples of 32 (ONEBIT_ERR_UNSUPPORTED otherwise), bucket <= 65536;
+ *   rows >= 1, cols >= 32, both below 2^24.  codes 16-byte aligned.
+ * The struct is a host struct, read during the call. */
+typedef struct {
+    const uint8_t *codes;
+    const float *bucket_min;
+    const float *bucket_max;
+    int64_t rows;
+    int64_t cols;
+    int bucket;
+    int bits;
+} qsdp_matrix_t;
+
+/* Products of `tokens` rows with coded weights, which are never decoded to memory:
+ *   qsdp_linear:       out_{t,o} = sum_i x_{t,i} w_{o,i}      (x [tokens][cols], out [tokens][rows])
+ *   qsdp_linear_grad:  dx_{t,i} = sum_o dy_{t,o} w_{o,i}      (dy [tokens][rows], dx [tokens][cols])
+ * The second is the gradient that the first hands back to its input; the weights' own is
+ * the plain product of dy and x.  From one token (a decoding step) to a training batch.
+ * x, dy: bf16 or fp16 (ONEBIT_ERR_UNSUPPORTED otherwise), row t at base + t * stride
+ * elements, 16-byte aligned base, stride a multiple of 8 (ONEBIT_ERR_ALIGN otherwise) and
+ * at least the row's length; what lies between two rows is never used.  out, dx: the same type,
+ * any stride of at least the row's length, which leaves what lies between two rows as it was.
+ * 0 <= tokens < 2^24; no tokens: the call does nothing.
+ * Sums are binary32.  Roundings before them: none in qsdp_linear with up to
+ * QSDP_LINEAR_EXACT_TOKENS tokens, where codes and minima enter apart; else of the weights
+ * to the type of x or dy, nearest even (for fp16, weights above 65504 become infinite).
+ * A value of x or dy that is not finite leaves nothing finite in its own row of the result and
+ * makes no difference to the others; a bucket whose minimum or maximum is not finite leaves
+ * nothing finite in the results that use its weights, and makes no difference to the others.
+ * (Sums of |x| over a row times 2^11 delta are to stay below 2^127.)
+ * workspace: qsdp_linear_workspace_bytes bytes (for either call), 16-byte aligned; what it
+ * holds before a call does not matter.  Calls that may overlap in time need one each, and
+ * so do two captured graphs that may be replayed at the same time.  (0 is returned for
+ * sizes that the calls refuse.)  The calls are not among the classes of the launch timing above. */
+#define QSDP_LINEAR_EXACT_TOKENS 64
+size_t qsdp_linear_workspace_bytes(int64_t tokens, int64_t rows, int64_t cols);
+onebit_status_t qsdp_linear(const void *x, onebit_dtype_t dtype, int64_t tokens, int64_t x_stride,
+                            const qsdp_matrix_t *w, void *out, int64_t out_stride, void *workspace,
+                            size_t workspace_bytes, void *stream);
+onebit_status_t qsdp_linear_grad(const void *dy, onebit_dtype_t dtype, int64_t tokens, int64_t dy_stride,
+                                 const qsdp_matrix_t *w, void *dx, int64_t dx_stride, void *workspace,
+                                 size_t workspace_bytes, void *stream);
+
 /* ------------------------------------------------------------------ coded key/value cache
  * A paged cache of attention keys and values held as signed levels, written, read
  * back and attended to in its coded form.  A row is the head_dim values of one token
@@ -458,6 +508,31 @@ onebit_status_t kvq_quantize(const void *k, const void *v, onebit_dtype_t dtype,
                              int64_t k_token_stride, int64_t k_head_stride, int64_t v_token_stride,
                              int64_t v_head_stride, const int64_t *slots, const kvq_cache_t *cache,
                              void *stream);
+
+/* Append new tokens to the cache with the rotation by their positions applied on the way:
+ * q_out = rotated q; the rotated keys and the values are coded as kvq_quantize codes them
+ * and written to slots[0 .. tokens).  Token i stands at position p = positions[i] (int64
+ * [tokens]).  rotary (fp32 [max_position][rot_dim], contiguous): row p holds cos and then sin
+ * of the rot_dim / 2 angles of position p, with any factor that the model puts on them.
+ * The first rot_dim values of a head are pairs (a, b), pair j of them values j and
+ * j + rot_dim / 2 (interleaved == 0) or 2 j and 2 j + 1 (interleaved != 0):
+ *   a' = fl32(a cos_j - b sin_j),   b' = fl32(b cos_j + a sin_j)
+ * formed in binary64, where the products are exact; the others stay as they are.  q_out is
+ * rounded once more to its type; keys go on to their codes in binary32.
+ * A position outside [0, max_position) turns its token's pairs into NaN: its rotated queries
+ * are NaN and its keys read back as NaN.  A slot outside the cache (padding) leaves the
+ * cache as it is; its token's queries are rotated all the same.
+ * No slot may occur twice in a call.  Tokens, k, v, slots: as in kvq_quantize, and q and
+ * q_out addressed as k is, of the same type.  q_out may be q itself (same strides) and must not
+ * overlap q otherwise.  q_heads from 0 (q and q_out are not used) to 32767; rot_dim a
+ * multiple of 16 from 16 to head_dim; max_position >= 1 and max_position * rot_dim < 2^47;
+ * rotary 16-byte aligned. */
+onebit_status_t kvq_append(const void *q, const void *k, const void *v, onebit_dtype_t dtype, int64_t tokens,
+                           int q_heads, int64_t q_token_stride, int64_t q_head_stride, int64_t k_token_stride,
+                           int64_t k_head_stride, int64_t v_token_stride, int64_t v_head_stride,
+                           const int64_t *positions, const float *rotary, int64_t max_position, int rot_dim,
+                           int interleaved, const int64_t *slots, const kvq_cache_t *cache, void *q_out,
+                           int64_t out_token_stride, int64_t out_head_stride, void *stream);
 
 /* Read the rows of slots[0 .. tokens) back (tokens below 2^26), rounded once more to bf16 or fp16 when
  * out_dtype is one of them: k_out, v_out [tokens][kv_heads][head_dim], contiguous,
