@@ -1,24 +1,10 @@
 // qsdp_linear.hip -- products of rows with a matrix kept in qsdp_quantize's codes, and the
 // gradient of their input.
 //   out_{t,o} = sum_i x_{t,i} w_{o,i},   dx_{t,i} = sum_o dy_{t,o} w_{o,i},   w = min_b + code * delta_b
-#include <hip/hip_runtime.h>
-
-#include "kvq_common.h"
+#include "qsdp_linear.h"
+#include "qsdp_rows.h"
 
 namespace onebit {
-
-struct LinearArgs {
-    const uint8_t *codes;
-    const float *lo, *hi;
-    int64_t rows, cols;  // of the matrix
-    int64_t bucket;
-    const uint16_t *x;  // [tokens][depth]
-    int64_t x_stride;
-    uint16_t *out;  // [tokens][width]
-    int64_t out_stride;
-    int64_t tokens;
-    void *workspace;
-};
 
 // One weight, as qsdp_dequantize decodes it.
 template <int BITS>
@@ -57,8 +43,37 @@ __global__ __launch_bounds__(256) void k_qsdp_linear_plain(LinearArgs a) {
     }
 }
 
+template <int GT, int BITS, int GROUPS, int NT, int MT, int WAVES, int SPLIT>
+static void launch_rows(const LinearArgs &a, hipStream_t s) {
+    constexpr int64_t each = 16 * NT * WAVES;
+    hipLaunchKernelGGL((k_qsdp_rows<GT, BITS, GROUPS, NT, MT, WAVES, SPLIT>), dim3((unsigned)((a.rows + each - 1) / each)),
+                       dim3(64 * WAVES * SPLIT), 0, s, a);
+}
+template <int GT, int BITS, int GROUPS>
+static void launch_rows_tiles(const LinearArgs &a, hipStream_t s) {
+    const bool wide = a.rows >= 64 * 256;
+    if (a.tokens <= 16) {
+        if (wide)
+            a.cols >= 32 * kRowsChunk ? launch_rows<GT, BITS, GROUPS, 1, 1, 4, 2>(a, s) : launch_rows<GT, BITS, GROUPS, 1, 1, 4, 1>(a, s);
+        else
+            a.cols >= 32 * kRowsChunk ? launch_rows<GT, BITS, GROUPS, 1, 1, 1, 8>(a, s) : launch_rows<GT, BITS, GROUPS, 1, 1, 2, 4>(a, s);
+    } else if (a.tokens <= 32) {
+        wide ? launch_rows<GT, BITS, GROUPS, 2, 2, 4, 2>(a, s) : launch_rows<GT, BITS, GROUPS, 1, 2, 2, 4>(a, s);
+    } else {
+        wide ? launch_rows<GT, BITS, GROUPS, 2, 4, 4, 2>(a, s) : launch_rows<GT, BITS, GROUPS, 1, 4, 4, 2>(a, s);
+    }
+}
+template <int GT, int BITS>
+static void launch_rows_groups(const LinearArgs &a, hipStream_t s) {
+    if (a.cols % kRowsChunk == 0 && a.bucket % kRowsChunk == 0)
+        launch_rows_tiles<GT, BITS, 1>(a, s);
+    else
+        launch_rows_tiles<GT, BITS, 4>(a, s);
+}
+
 template <int GT, int BITS, bool GRAD>
 static void launch(const LinearArgs &a, hipStream_t s) {
+    if (!GRAD && a.tokens <= QSDP_LINEAR_EXACT_TOKENS) return launch_rows_groups<GT, BITS>(a, s);
     const int64_t width = GRAD ? a.cols : a.rows;
     // at most 65535 workgroups along y
     const int64_t most = 65535 * 32;
@@ -113,6 +128,7 @@ static onebit_status_t linear(const void *x, onebit_dtype_t dtype, int64_t token
     a.rows = w->rows;
     a.cols = w->cols;
     a.bucket = w->bucket;
+    a.bucket_magic = (uint32_t)(((uint64_t{1} << 32) + w->bucket / 32 - 1) / (w->bucket / 32));
     a.x = static_cast<const uint16_t *>(x);
     a.x_stride = tokens > 1 ? x_stride : 0;
     a.out = static_cast<uint16_t *>(out);
