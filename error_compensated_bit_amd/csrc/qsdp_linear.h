@@ -3,7 +3,7 @@
 
 #include <hip/hip_runtime.h>
 
-#include "kvq_common.h"
+#include "kvq_attention.h"
 
 namespace onebit {
 
@@ -22,6 +22,16 @@ struct LinearArgs {
     int64_t tokens;
     void *workspace;
 };
+
+typedef __bf16 bf16x8_v __attribute__((ext_vector_type(8)));
+
+template <int GT>
+__device__ __forceinline__ f32x4_v product16(const u32x4_v a, const u32x4_v b, f32x4_v c) {
+    if (GT == kGradBF16)
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_v, a), __builtin_bit_cast(bf16x8_v, b), c,
+                                                       0, 0, 0);
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8_v, a), __builtin_bit_cast(f16x8_v, b), c, 0, 0, 0);
+}
 
 // The bucket of the flat vector's 32-value part p (p < 2^43), and the part's place in it.
 struct Bucket {

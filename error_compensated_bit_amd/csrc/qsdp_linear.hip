@@ -1,47 +1,13 @@
 // qsdp_linear.hip -- products of rows with a matrix kept in qsdp_quantize's codes, and the
 // gradient of their input.
 //   out_{t,o} = sum_i x_{t,i} w_{o,i},   dx_{t,i} = sum_o dy_{t,o} w_{o,i},   w = min_b + code * delta_b
+#include <algorithm>
+
 #include "qsdp_linear.h"
 #include "qsdp_rows.h"
+#include "qsdp_tile.h"
 
 namespace onebit {
-
-// One weight, as qsdp_dequantize decodes it.
-template <int BITS>
-__device__ __forceinline__ float weight_at(const LinearArgs &a, int64_t i) {
-    const int64_t b = i / a.bucket;
-    const uint32_t c = BITS == 8 ? a.codes[i] : (a.codes[i >> 1] >> (4 * (i & 1))) & 15u;
-    const float lo = a.lo[b], delta = __fdiv_rn(sub_rn(a.hi[b], lo), (float)((1 << BITS) - 1));
-    return add_rn(lo, mul_rn((float)(int)c, delta));
-}
-
-// 32 x 32 results by 256 threads, binary32 throughout.
-template <int GT, int BITS, bool GRAD>
-__global__ __launch_bounds__(256) void k_qsdp_linear_plain(LinearArgs a) {
-    __shared__ float xs[32][33], ws[32][33];
-    const int64_t depth = GRAD ? a.rows : a.cols, width = GRAD ? a.cols : a.rows;
-    const int64_t t0 = (int64_t)blockIdx.y * 32, o0 = (int64_t)blockIdx.x * 32;
-    const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
-    float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    for (int64_t d0 = 0; d0 < depth; d0 += 32) {
-        for (int r = ty; r < 32; r += 8) {
-            const int64_t t = t0 + r, d = d0 + tx;
-            xs[r][tx] = t < a.tokens && d < depth ? half_bits_to_float<GT>(a.x[t * a.x_stride + d]) : 0.0f;
-            // linear: row o0 + r of the matrix, column d0 + tx; gradient: row d0 + r, column o0 + tx
-            const int64_t row = (GRAD ? d0 : o0) + r, col = (GRAD ? o0 : d0) + tx;
-            ws[r][tx] = row < a.rows && col < a.cols ? weight_at<BITS>(a, row * a.cols + col) : 0.0f;
-        }
-        __syncthreads();
-        for (int d = 0; d < 32; ++d)
-            for (int j = 0; j < 4; ++j)
-                acc[j] = __fmaf_rn(xs[ty + 8 * j][d], GRAD ? ws[d][tx] : ws[tx][d], acc[j]);
-        __syncthreads();
-    }
-    for (int j = 0; j < 4; ++j) {
-        const int64_t t = t0 + ty + 8 * j, o = o0 + tx;
-        if (t < a.tokens && o < width) a.out[t * a.out_stride + o] = (uint16_t)round_pair<GT>(acc[j], 0.0f);
-    }
-}
 
 template <int GT, int BITS, int GROUPS, int NT, int MT, int WAVES, int SPLIT>
 static void launch_rows(const LinearArgs &a, hipStream_t s) {
@@ -71,20 +37,52 @@ static void launch_rows_groups(const LinearArgs &a, hipStream_t s) {
         launch_rows_tiles<GT, BITS, 4>(a, s);
 }
 
+using BigTile = TileShape<256, 256, 128, 64>;
+using SmallTile = TileShape<128, 128, 64, 64>;
+
+// How a product is cut up: its tiles and how many workgroups share the depth of each.
+struct TilePlan {
+    bool big;
+    int64_t tiles_m, tiles_n;
+    int splits;
+    size_t bytes;  // of partial results
+};
+static TilePlan tile_plan(int64_t tokens, int64_t width, int64_t depth) {
+    TilePlan p;
+    const int64_t big = ((tokens + 255) / 256) * ((width + 255) / 256);
+    p.big = big >= 192;
+    const int64_t side = p.big ? 256 : 128, room = p.big ? 256 : 512, steps = (depth + kTileDepth - 1) / kTileDepth;
+    p.tiles_m = (tokens + side - 1) / side;
+    p.tiles_n = (width + side - 1) / side;
+    const int64_t tiles = p.tiles_m * p.tiles_n;
+    p.splits = (int)std::max<int64_t>(1, std::min({room / tiles, steps / 4, (int64_t)64}));
+    p.bytes = p.splits > 1 ? (size_t)tiles * p.splits * side * side * sizeof(float) : 0;
+    return p;
+}
+
+template <int GT, int BITS, bool GRAD, class S>
+static void launch_tile(const TileArgs &a, hipStream_t s) {
+    const int64_t tiles = (int64_t)a.tiles_m * a.tiles_n;
+    hipLaunchKernelGGL((k_qsdp_tile<GT, BITS, GRAD, S>), dim3((unsigned)(tiles * a.splits)), dim3(S::kThreads), 0, s, a);
+    if (a.splits > 1)
+        hipLaunchKernelGGL((k_qsdp_tile_join<GT, S>), dim3((unsigned)((tiles * S::kWaves * S::kFrags + 3) / 4)), dim3(256), 0,
+                           s, a);
+}
+
 template <int GT, int BITS, bool GRAD>
-static void launch(const LinearArgs &a, hipStream_t s) {
-    if (!GRAD && a.tokens <= QSDP_LINEAR_EXACT_TOKENS) return launch_rows_groups<GT, BITS>(a, s);
-    const int64_t width = GRAD ? a.cols : a.rows;
-    // at most 65535 workgroups along y
-    const int64_t most = 65535 * 32;
-    for (int64_t t = 0; t < a.tokens; t += most) {
-        LinearArgs x = a;
-        x.x += t * a.x_stride;
-        x.out += t * a.out_stride;
-        x.tokens = a.tokens - t < most ? a.tokens - t : most;
-        hipLaunchKernelGGL((k_qsdp_linear_plain<GT, BITS, GRAD>),
-                           dim3((unsigned)((width + 31) / 32), (unsigned)((x.tokens + 31) / 32)), dim3(256), 0, s, x);
-    }
+static void launch(const LinearArgs &l, hipStream_t s) {
+    if (!GRAD && l.tokens <= QSDP_LINEAR_EXACT_TOKENS) return launch_rows_groups<GT, BITS>(l, s);
+    TileArgs a{};
+    a.l = l;
+    a.depth = GRAD ? l.rows : l.cols;
+    a.width = GRAD ? l.cols : l.rows;
+    const TilePlan p = tile_plan(l.tokens, a.width, a.depth);
+    a.tiles_m = (int32_t)p.tiles_m;
+    a.tiles_n = (int32_t)p.tiles_n;
+    a.splits = p.splits;
+    a.steps = (int32_t)((a.depth + kTileDepth - 1) / kTileDepth);
+    a.partial = static_cast<float *>(l.workspace);
+    p.big ? launch_tile<GT, BITS, GRAD, BigTile>(a, s) : launch_tile<GT, BITS, GRAD, SmallTile>(a, s);
 }
 template <bool GRAD>
 static void dispatch(onebit_dtype_t dtype, int bits, const LinearArgs &a, hipStream_t s) {
@@ -99,7 +97,9 @@ constexpr int64_t kLinearMost = 1 << 24;  // tokens, rows and columns are below
 static size_t linear_workspace(int64_t tokens, int64_t rows, int64_t cols) {
     if (tokens < 0 || tokens >= kLinearMost || rows < 1 || rows >= kLinearMost || cols < 32 || cols >= kLinearMost || cols % 32)
         return 0;
-    return 16;
+    if (tokens == 0) return 16;
+    const size_t linear = tokens > QSDP_LINEAR_EXACT_TOKENS ? tile_plan(tokens, rows, cols).bytes : 0;
+    return std::max({(size_t)16, linear, tile_plan(tokens, cols, rows).bytes});
 }
 
 template <bool GRAD>

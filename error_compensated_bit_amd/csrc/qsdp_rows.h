@@ -15,23 +15,12 @@
 // add up in LDS at the end.
 #pragma once
 
-#include "kvq_attention.h"
 #include "qsdp_linear.h"
 
 namespace onebit {
 
 constexpr int kRowsChunk = 128;  // columns of a step
 constexpr int kRowsAhead = 4;    // steps under way
-
-typedef __bf16 bf16x8_v __attribute__((ext_vector_type(8)));
-
-template <int GT>
-__device__ __forceinline__ f32x4_v product16(const u32x4_v a, const u32x4_v b, f32x4_v c) {
-    if (GT == kGradBF16)
-        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_v, a), __builtin_bit_cast(bf16x8_v, b), c,
-                                                       0, 0, 0);
-    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8_v, a), __builtin_bit_cast(f16x8_v, b), c, 0, 0, 0);
-}
 
 // What stands in front of a code in the operand, and so in every sum over codes.
 template <int GT, int BITS>

@@ -32,9 +32,11 @@ def product(x, w, delta, bits, dtype, exact):
 
     The tolerance counts, with A = sum |x| |w|, S = sum |x|:
       - the result's own rounding: half a step of the result (of the smallest normal number at least);
-      - `exact` false: each weight's rounding to the type, half a step of it each: as many independent
-        errors of at most half a step of |x w|, eight times the root of their squares' sum; weights
-        of fp16 below 2^-14 are off by 2^-25;
+      - `exact` false: each weight's rounding to the type, half a step of it each: half a step of A.
+        (No less: a bucket has 2^bits different weights, so the errors of equal codes are equal and do not
+        average out.  With one bucket a row, 130 of 2080 weights share one error, and where x has a mean of
+        half its spread their sum is 130 / 2 spreads and not sqrt(130).)  Weights of fp16 below 2^-14
+        are off by 2^-25;
       - the sums in fp32.  Where codes and minima enter apart (`exact`), a code stands for at most
         R = 32 (4 bits, an offset of 16 in front) or 256 (8 bits) steps of its bucket, so terms and
         partial sums are within B = A + R sum |x| delta, else within A.  depth + 64 roundings of 2^-24,
@@ -48,7 +50,7 @@ def product(x, w, delta, bits, dtype, exact):
     if exact:
         big = big + (32.0 if bits == 4 else 256.0) * (a @ delta)
     else:
-        tol = tol + 8.0 * half * ((a * a) @ (w * w)).sqrt()
+        tol = tol + half * big
         if dtype == torch.float16:
             tol = tol + 2.0 ** -25 * a.sum(1, keepdim=True)
     return y, tol + 8.0 * (x.shape[1] + 64) ** 0.5 * 2.0 ** -24 * big

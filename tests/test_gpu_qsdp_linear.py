@@ -108,6 +108,24 @@ def test_products_within_the_counted_roundings(op, bits, rows, cols, bucket, dty
         assert torch.all(off <= 1.0), (tokens, float(off.max()))
 
 
+@pytest.mark.parametrize("op,rows,cols", [("linear", 3333, 160), ("linear", 3400, 1600), ("grad", 133, 3360), ("grad", 1601, 3392)])
+@pytest.mark.parametrize("bits,bucket", [(4, 1024), (4, 32), (8, 96), (8, 1600)])
+@pytest.mark.parametrize("dtype", [BF16, F16])
+def test_many_tokens(op, rows, cols, bits, bucket, dtype):
+    """Products with enough tiles for the largest ones, whole numbers and others."""
+    tokens = 4100
+    g = gen("many", op, rows, bits)
+    depth = cols if op == "linear" else rows
+    weights = coded(rows, cols, bucket, bits, g, whole=True)
+    x = torch.randint(-2, 3, (tokens, depth), generator=g).to(dtype)
+    want = expect(op, x.to(DEV), weights, rows, cols, bucket, bits)[0].float().to(dtype)
+    assert torch.equal(run(op, padded(x), dev(weights), rows, cols, bucket, bits), want)
+    weights = coded(rows, cols, bucket, bits, g)
+    x = torch.randn(tokens, depth, generator=g).to(dtype)
+    want, tol = expect(op, x.to(DEV), weights, rows, cols, bucket, bits)
+    assert torch.all((run(op, padded(x), dev(weights), rows, cols, bucket, bits).double() - want).abs() <= tol)
+
+
 @pytest.mark.parametrize("tokens", [5, 40, 130])
 @pytest.mark.parametrize("bits", [4, 8])
 def test_gradient_is_the_products_differences(tokens, bits):
