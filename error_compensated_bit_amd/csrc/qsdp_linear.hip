@@ -37,8 +37,8 @@ static void launch_rows_groups(const LinearArgs &a, hipStream_t s) {
         launch_rows_tiles<GT, BITS, 4>(a, s);
 }
 
-using BigTile = TileShape<256, 256, 128, 64>;
-using SmallTile = TileShape<128, 128, 64, 64>;
+using BigTile = TileShape<256, 256, 128, 64, 1, 1>;
+using SmallTile = TileShape<128, 128, 64, 64, 2, 2>;
 
 // How a product is cut up: its tiles and how many workgroups share the depth of each.
 struct TilePlan {
@@ -51,7 +51,7 @@ static TilePlan tile_plan(int64_t tokens, int64_t width, int64_t depth) {
     TilePlan p;
     const int64_t big = ((tokens + 255) / 256) * ((width + 255) / 256);
     p.big = big >= 192;
-    const int64_t side = p.big ? 256 : 128, room = p.big ? 256 : 512, steps = (depth + kTileDepth - 1) / kTileDepth;
+    const int64_t side = p.big ? 256 : 128, room = 256, steps = (depth + kTileDepth - 1) / kTileDepth;
     p.tiles_m = (tokens + side - 1) / side;
     p.tiles_n = (width + side - 1) / side;
     const int64_t tiles = p.tiles_m * p.tiles_n;
@@ -63,7 +63,7 @@ static TilePlan tile_plan(int64_t tokens, int64_t width, int64_t depth) {
 template <int GT, int BITS, bool GRAD, class S>
 static void launch_tile(const TileArgs &a, hipStream_t s) {
     const int64_t tiles = (int64_t)a.tiles_m * a.tiles_n;
-    hipLaunchKernelGGL((k_qsdp_tile<GT, BITS, GRAD, S>), dim3((unsigned)(tiles * a.splits)), dim3(S::kThreads), 0, s, a);
+    hipLaunchKernelGGL((k_qsdp_tile<GT, BITS, GRAD, S>), dim3((unsigned)(tiles * a.splits)), dim3(S::kThreads * S::kGroups), 0, s, a);
     if (a.splits > 1)
         hipLaunchKernelGGL((k_qsdp_tile_join<GT, S>), dim3((unsigned)((tiles * S::kWaves * S::kFrags + 3) / 4)), dim3(256), 0,
                            s, a);
@@ -115,7 +115,7 @@ static onebit_status_t linear(const void *x, onebit_dtype_t dtype, int64_t token
     if (tokens == 0) return ONEBIT_OK;
     const int64_t depth = GRAD ? w->rows : w->cols, width = GRAD ? w->cols : w->rows;
     if (!x || !out || !workspace || !w->codes || !w->bucket_min || !w->bucket_max) return ONEBIT_ERR_INVALID;
-    if (tokens > 1 && (x_stride < depth || out_stride < width || x_stride >= int64_t{1} << 32 || out_stride >= int64_t{1} << 32))
+    if (tokens > 1 && (x_stride < depth || out_stride < width || x_stride >= int64_t{1} << 23 || out_stride >= int64_t{1} << 32))
         return ONEBIT_ERR_INVALID;
     if (workspace_bytes < linear_workspace(tokens, w->rows, w->cols)) return ONEBIT_ERR_INVALID;
     if (!aligned16(x) || (tokens > 1 && x_stride % 8) || !aligned_to(out, 2) || !aligned16(workspace) || !aligned16(w->codes) ||

@@ -4,11 +4,13 @@
 // A workgroup has TM x TN results and goes through the depth in steps of 64.  A step's x
 // and its weights, expanded once for all TM rows and rounded to x's type, lie in LDS twice over:
 // while one is multiplied the next is written and the one after that is on its way from memory.
-// The upper half of the waves writes first and multiplies then, the lower half the other way
-// round, so that of two waves on a SIMD one keeps the matrix cores busy while the other expands.
+// Half of the waves write first and multiply then, the others the other way round, so that of
+// two waves on a SIMD one keeps the matrix cores busy while the other expands.
 //
 // LDS: rows of 64 values (128 bytes) of x and of weights, the 16-byte pieces of row r in the order
-// p ^ swizzle(r); an operand of v_mfma_f32_16x16x32 is one piece of 16 rows.  Weights are the first
+// p ^ x_swizzle(r) or p ^ w_swizzle(r), so that what eight lanes read or write at once lies in
+// different banks, while rows a multiple of 32 apart (of 16, for x) have one order: their
+// addresses differ by a constant.  An operand of v_mfma_f32_16x16x32 is one piece of 16 rows.  Weights are the first
 // operand, so that a lane holds four neighbouring results of one row of x.
 #pragma once
 
@@ -18,12 +20,16 @@ namespace onebit {
 
 constexpr int kTileDepth = 64;
 
-template <int TM_, int TN_, int WM_, int WN_>
+// TM x TN results of a workgroup, WM x WN of a wave; GROUPS of waves share the depth, each with
+// buffers of its own; AHEAD steps of a group are on their way from memory.
+template <int TM_, int TN_, int WM_, int WN_, int GROUPS, int AHEAD>
 struct TileShape {
-    static constexpr int TM = TM_, TN = TN_, WM = WM_, WN = WN_;
+    static constexpr int TM = TM_, TN = TN_, WM = WM_, WN = WN_, kGroups = GROUPS, kAhead = AHEAD;
+    // of a group
     static constexpr int kWaves = (TM / WM) * (TN / WN), kThreads = 64 * kWaves;
     static constexpr int kXPieces = TM * 8 / kThreads;  // of a thread
     static constexpr int kFrags = (WM / 16) * (WN / 16);
+    static constexpr int kOccupancy = kWaves * GROUPS / 4;  // waves on a SIMD
     static_assert(kThreads == 2 * TN, "a thread expands 32 codes of a step");
 };
 
@@ -36,7 +42,8 @@ struct TileArgs {
     float *partial;      // [tile][split][wave][frag][lane][4] where splits > 1
 };
 
-__device__ __forceinline__ int tile_swizzle(int r) { return (r ^ (r >> 3)) & 7; }
+__device__ __forceinline__ int x_swizzle(int r) { return (r ^ ((r >> 3) & 1)) & 7; }
+__device__ __forceinline__ int w_swizzle(int r) { return (r ^ ((r >> 3) & 3)) & 7; }
 
 // Two weights of one row, rounded once more to x's type.
 template <int GT>
@@ -60,11 +67,14 @@ __device__ __forceinline__ void store_results(const TileArgs &a, int64_t t, int6
 }
 
 template <int GT, int BITS, bool GRAD, class S>
-__global__ __launch_bounds__(S::kThreads) void k_qsdp_tile(TileArgs a) {
+__global__ __launch_bounds__(S::kThreads * S::kGroups, S::kOccupancy) void k_qsdp_tile(TileArgs a) {
     constexpr int kXBytes = S::TM * 128, kWBytes = S::TN * 128;
     constexpr int kScaleBytes = GRAD ? S::kThreads * 8 : 0;
-    __shared__ __attribute__((aligned(16))) char s_mem[2 * (kXBytes + kWBytes + kScaleBytes)];
-    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    constexpr int kGroupBytes = 2 * (kXBytes + kWBytes + kScaleBytes);
+    __shared__ __attribute__((aligned(16))) char s_all[S::kGroups * kGroupBytes];
+    const int group = S::kGroups == 1 ? 0 : __builtin_amdgcn_readfirstlane(threadIdx.x / S::kThreads);
+    char *s_mem = s_all + group * kGroupBytes;
+    const int tid = threadIdx.x - group * S::kThreads, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int n = lane & 15, g = lane >> 4;
 
     // ---- which tile, which part of the depth.  Workgroups go round the XCDs: each XCD takes consecutive ones.
@@ -76,60 +86,69 @@ __global__ __launch_bounds__(S::kThreads) void k_qsdp_tile(TileArgs a) {
     const int split = at % a.splits, tile = at / a.splits;
     const int tm = tile % a.tiles_m, tn = tile / a.tiles_m;
     const int64_t t0 = (int64_t)tm * S::TM, o0 = (int64_t)tn * S::TN;
-    const int begin = (int)((int64_t)a.steps * split / a.splits), end = (int)((int64_t)a.steps * (split + 1) / a.splits);
+    // this group's steps; every group of the workgroup goes through as many
+    const int first = (int)((int64_t)a.steps * split / a.splits), behind = (int)((int64_t)a.steps * (split + 1) / a.splits);
+    const int each = (behind - first + S::kGroups - 1) / S::kGroups;
+    const int begin = min(first + group * each, behind), end = min(begin + each, behind);
     const int whole = (int)(a.depth / kTileDepth);  // steps that are full
 
-    // ---- x: rows (tid >> 3) + kThreads / 8 * m, piece tid & 7
-    const uint16_t *x[S::kXPieces];
+    const auto first_of = [&](int64_t base, int64_t count, int r) { return (uint32_t)(min(base + r, count - 1) - base); };
+
+    // ---- x: rows (tid >> 3) + kThreads / 8 * m, piece tid & 7; by offsets from the tile's first row, which
+    // fit 32 bits (256 rows, strides below 2^23)
+    const char *x = reinterpret_cast<const char *>(a.l.x + t0 * a.l.x_stride);
+    uint32_t x_off[S::kXPieces];
 #pragma unroll
     for (int m = 0; m < S::kXPieces; ++m)
-        x[m] = a.l.x + min(t0 + (tid >> 3) + S::kThreads / 8 * m, a.l.tokens - 1) * a.l.x_stride + 8 * (tid & 7);
-    u32x4_v xr[S::kXPieces];
+        x_off[m] = first_of(t0, a.l.tokens, (tid >> 3) + S::kThreads / 8 * m) * (2 * (uint32_t)a.l.x_stride) + 16 * (tid & 7);
+    constexpr int kA = S::kAhead;
+    u32x4_v xr[kA][S::kXPieces];
 
     // ---- codes
-    const int64_t row_parts = a.l.cols >> 5;
-    const int64_t row_bytes = row_parts * (4 * BITS);
-    const uint32_t bucket_parts = (uint32_t)a.l.bucket >> 5;
-    constexpr int kCodeWords = GRAD ? 8 : BITS;  // loads of 4 rows' columns, or words of 32 codes
-    uint32_t code[kCodeWords];
-    float lo, hi;
-    const uint8_t *codes;
-    // linear: the row's first bucket and the row's place in it; gradient: those of the entry's next part
-    int64_t bucket;
-    uint32_t part;
-    // linear: thread's row and half of a step.  gradient: rows 8 (tid / (TN / 4)) + 0 .. 7 of a step, columns
+    const uint32_t row_parts = (uint32_t)(a.l.cols >> 5), bucket_parts = (uint32_t)a.l.bucket >> 5;
+    const uint32_t row_bytes = row_parts * (4 * BITS);
+    constexpr int kCodeWords = GRAD ? 8 : BITS;  // columns of eight rows, or words of 32 codes
+    uint32_t code[kA][kCodeWords];
+    float lo[kA], hi[kA];
+    // linear: this thread's row and half of a step.  gradient: rows 8 (tid / (TN / 4)) + 0 .. 7 of a step, columns
     // 4 (tid % (TN / 4)) + 0 .. 3, and an entry of the step's table of minima and steps: row tid / (TN / 32),
     // columns 32 (tid % (TN / 32)) + 0 .. 31.
     const int c_row = GRAD ? 8 * (tid / (S::TN / 4)) : tid >> 1, c_col = GRAD ? 4 * (tid % (S::TN / 4)) : 32 * (tid & 1);
     const int e_row = tid / (S::TN / 32), e_part = tid % (S::TN / 32);
-    uint32_t step_parts = 0;
-    int64_t step_buckets = 0;
+    const uint8_t *codes = a.l.codes;
+    const float *los = a.l.lo, *his = a.l.hi;
+    uint32_t code_off, part, step_parts = 0;  // part: in front of the thread's next part in its bucket
+    int64_t bucket = 0, step_buckets = 0;
     if (GRAD) {
-        codes = a.l.codes + (min(o0 + c_col, a.l.cols - 4) * BITS >> 3);
-        const int64_t p = min((o0 >> 5) + e_part, row_parts - 1);
-        const Bucket b = bucket_of(((int64_t)begin * kTileDepth + e_row) * row_parts + p, bucket_parts);
+        codes += o0 * BITS >> 3;
+        code_off = (uint32_t)c_row * row_bytes + (first_of(o0 >> 2, a.l.cols >> 2, c_col >> 2) * BITS >> 1);
+        const int64_t p = (int64_t)begin * kTileDepth + e_row;
+        const Bucket b = bucket_of(p * row_parts + min((uint32_t)(o0 >> 5) + e_part, row_parts - 1), bucket_parts);
         bucket = b.index;
         part = b.part;
-        const Bucket d = bucket_of(kTileDepth * row_parts, bucket_parts);
+        const Bucket d = bucket_of((int64_t)kTileDepth * row_parts, bucket_parts);
         step_buckets = d.index;
         step_parts = d.part;
     } else {
-        const int64_t row = min(o0 + c_row, a.l.rows - 1);
-        codes = a.l.codes + row * row_bytes;
-        const Bucket b = bucket_of(row * row_parts, bucket_parts);
-        bucket = b.index;
-        part = b.part;
+        const uint32_t r = first_of(o0, a.l.rows, c_row);
+        const Bucket b = bucket_of(o0 * row_parts, bucket_parts);
+        codes += o0 * row_bytes;
+        los += b.index;
+        his += b.index;
+        code_off = r * row_bytes;
+        const uint32_t parts = b.part + r * row_parts;
+        bucket = parts / bucket_parts;
+        part = parts - (uint32_t)bucket * bucket_parts;
     }
 
     // minima and maxima of step s (gradient: to be called for every step in turn)
-    const auto load_scales = [&](int s) {
+    const auto load_scales = [&](int s, int slot) {
         if (GRAD) {
             const bool in = s < end && (int64_t)s * kTileDepth + e_row < a.l.rows;
-            lo = hi = 0.0f;
-            if (in) {
-                lo = a.l.lo[bucket];
-                hi = a.l.hi[bucket];
-            }
+            const int64_t b = in ? bucket : 0;
+            lo[slot] = los[b];
+            hi[slot] = his[b];
+            if (!in) lo[slot] = hi[slot] = 0.0f;  // behind the last row: weights of 0
             bucket += step_buckets;
             part += step_parts;
             if (part >= bucket_parts) {
@@ -137,45 +156,58 @@ __global__ __launch_bounds__(S::kThreads) void k_qsdp_tile(TileArgs a) {
                 ++bucket;
             }
         } else {
-            const int c = s * 2 + (tid & 1);
-            const uint32_t k = part + (uint32_t)min((int64_t)c, row_parts - 1);
-            const int64_t b = bucket + (bucket_parts == 1 ? k : __umulhi(k, a.l.bucket_magic));
-            lo = a.l.lo[b];
-            hi = a.l.hi[b];
-            if (c >= row_parts) lo = hi = 0.0f;  // behind the row's end: weights of 0
+            const uint32_t c = (uint32_t)s * 2 + (tid & 1), k = part + min(c, row_parts - 1);
+            const uint32_t b = (uint32_t)bucket + (bucket_parts == 1 ? k : __umulhi(k, a.l.bucket_magic));
+            lo[slot] = los[b];
+            hi[slot] = his[b];
+            if (c >= row_parts) lo[slot] = hi[slot] = 0.0f;  // behind the row's end: weights of 0
         }
     };
-    const auto load = [&](int s) {
+    // (steps behind the last are the last one again, not used: a branch around the loads would make the
+    // compiler wait for all that are under way)
+    const auto load = [&](int step, int slot) {
+        const int s = max(min(step, end - 1), first);
         const int64_t d0 = (int64_t)s * kTileDepth;
+        if (!GRAD) load_scales(s, slot);
         if (s < whole) {
 #pragma unroll
-            for (int m = 0; m < S::kXPieces; ++m) xr[m] = *reinterpret_cast<const u32x4_v *>(x[m] + d0);
+            for (int m = 0; m < S::kXPieces; ++m)
+                xr[slot][m] = *reinterpret_cast<const u32x4_v *>(x + 2 * d0 + x_off[m]);
         } else {
             // the depth's end: value by value, zeros behind it
 #pragma unroll
             for (int m = 0; m < S::kXPieces; ++m) {
-                uint32_t v[4] = {0u, 0u, 0u, 0u};
-                for (int k = 0; k < 8; ++k)
-                    if (d0 + 8 * (tid & 7) + k < a.depth) v[k >> 1] |= (uint32_t)x[m][d0 + k] << (16 * (k & 1));
-                xr[m] = (u32x4_v){v[0], v[1], v[2], v[3]};
+                const uint16_t *p = reinterpret_cast<const uint16_t *>(x + 2 * d0 + x_off[m]);
+                uint32_t v[8];
+#pragma unroll
+                for (int k = 0; k < 8; ++k) v[k] = d0 + 8 * (tid & 7) + k < a.depth ? p[k] : 0u;
+                xr[slot][m] = (u32x4_v){v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16, v[6] | v[7] << 16};
             }
         }
         if (GRAD) {
+            const uint8_t *p = codes + d0 * row_bytes;
+            const auto code_at = [&](const uint8_t *q) -> uint32_t {
+                return BITS == 4 ? *reinterpret_cast<const uint16_t *>(q) : *reinterpret_cast<const uint32_t *>(q);
+            };
+            if (s < whole) {
 #pragma unroll
-            for (int r = 0; r < 8; ++r) {
-                // (behind the last row: the last one, times a table's zeros)
-                const uint8_t *p = codes + min(d0 + c_row + r, a.l.rows - 1) * row_bytes;
-                code[r] = BITS == 4 ? *reinterpret_cast<const uint16_t *>(p) : *reinterpret_cast<const uint32_t *>(p);
+                for (int r = 0; r < 8; ++r) code[slot][r] = code_at(p + (uint64_t)r * row_bytes + code_off);
+            } else {
+                // (behind the last row: the last one, times the table's zeros)
+                const int last = (int)(a.l.rows - d0) - 1;
+#pragma unroll
+                for (int r = 0; r < 8; ++r)
+                    code[slot][r] = code_at(p + (code_off - (uint32_t)(c_row - min(c_row + r, last)) * row_bytes));
             }
         } else {
-            const int64_t d = min(d0 + c_col, a.l.cols - 32);
+            const uint32_t off = code_off + (min((uint32_t)s * kTileDepth + c_col, row_parts * 32 - 32) * BITS >> 3);
 #pragma unroll
             for (int k = 0; k < BITS / 4; ++k) {
-                const uint4 v = *reinterpret_cast<const uint4 *>(codes + (d * BITS >> 3) + 16 * k);
-                code[4 * k] = v.x;
-                code[4 * k + 1] = v.y;
-                code[4 * k + 2] = v.z;
-                code[4 * k + 3] = v.w;
+                const uint4 v = *reinterpret_cast<const uint4 *>(codes + off + 16 * k);
+                code[slot][4 * k] = v.x;
+                code[slot][4 * k + 1] = v.y;
+                code[slot][4 * k + 2] = v.z;
+                code[slot][4 * k + 3] = v.w;
             }
         }
     };
@@ -185,58 +217,50 @@ __global__ __launch_bounds__(S::kThreads) void k_qsdp_tile(TileArgs a) {
     const auto table_at = [&](int buffer) {
         return reinterpret_cast<float2 *>(s_mem + 2 * (kXBytes + kWBytes) + buffer * kScaleBytes);
     };
-    const auto keep_table = [&](int buffer) { table_at(buffer)[tid] = make_float2(lo, bucket_delta<BITS>(lo, hi)); };
+    const auto keep_table = [&](int buffer, int slot) {
+        table_at(buffer)[tid] = make_float2(lo[slot], bucket_delta<BITS>(lo[slot], hi[slot]));
+    };
     const auto byte_of = [](uint32_t w, int k) -> float { return (float)((w >> (8 * k)) & 255u); };
 
-    // x and weights of the step that has been loaded into buffer s & 1
-    const auto store = [&](int s) {
-        u32x4_v *xs = x_at(s & 1), *ws = w_at(s & 1);
+    // x and weights of the step in `slot` into `buffer`
+    const auto store = [&](int buffer, int slot) {
+        u32x4_v *xs = x_at(buffer) + 8 * (tid >> 3) + ((tid & 7) ^ x_swizzle(tid >> 3)), *ws = w_at(buffer);
 #pragma unroll
-        for (int m = 0; m < S::kXPieces; ++m) {
-            const int r = (tid >> 3) + S::kThreads / 8 * m;
-            xs[8 * r + ((tid & 7) ^ tile_swizzle(r))] = xr[m];
-        }
+        for (int m = 0; m < S::kXPieces; ++m) xs[S::kThreads * m] = xr[slot][m];
         if (GRAD) {
-            float w[8][4];
+            float2 e[8];
 #pragma unroll
-            for (int r = 0; r < 8; ++r) {
-                const float2 e = table_at(s & 1)[(c_row + r) * (S::TN / 32) + (c_col >> 5)];
-                float c[4];
-                if (BITS == 4) {
-                    // nibbles 0 2 and 1 3 as bytes
-                    const uint32_t even = code[r] & 0x0f0fu, odd = (code[r] >> 4) & 0x0f0fu;
-                    c[0] = byte_of(even, 0); c[1] = byte_of(odd, 0); c[2] = byte_of(even, 1); c[3] = byte_of(odd, 1);
-                } else {
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) c[k] = byte_of(code[r], k);
-                }
-#pragma unroll
-                for (int k = 0; k < 4; ++k) w[r][k] = __fmaf_rn(c[k], e.y, e.x);
-            }
+            for (int r = 0; r < 8; ++r) e[r] = table_at(buffer)[(c_row + r) * (S::TN / 32) + (c_col >> 5)];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 const int o = c_col + k;
-                ws[8 * o + ((c_row >> 3) ^ tile_swizzle(o))] =
-                    (u32x4_v){round_pair<GT>(w[0][k], w[1][k]), round_pair<GT>(w[2][k], w[3][k]),
-                              round_pair<GT>(w[4][k], w[5][k]), round_pair<GT>(w[6][k], w[7][k])};
+                float w[8];
+#pragma unroll
+                for (int r = 0; r < 8; ++r) {
+                    const uint32_t c = code[slot][r];
+                    w[r] = __fmaf_rn((float)(BITS == 4 ? (c >> (4 * k)) & 15u : (c >> (8 * k)) & 255u), e[r].y, e[r].x);
+                }
+                ws[8 * o + ((c_row >> 3) ^ w_swizzle(o))] =
+                    (u32x4_v){round_pair<GT>(w[0], w[1]), round_pair<GT>(w[2], w[3]), round_pair<GT>(w[4], w[5]),
+                              round_pair<GT>(w[6], w[7])};
             }
         } else {
-            const float delta = bucket_delta<BITS>(lo, hi);
+            const float delta = bucket_delta<BITS>(lo[slot], hi[slot]);
 #pragma unroll
             for (int p = 0; p < 4; ++p) {
                 u32x4_v v;
                 if (BITS == 4) {
-                    const uint32_t even = code[p] & 0x0f0f0f0fu, odd = (code[p] >> 4) & 0x0f0f0f0fu;
+                    const uint32_t even = code[slot][p] & 0x0f0f0f0fu, odd = (code[slot][p] >> 4) & 0x0f0f0f0fu;
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) v[k] = weight_pair<GT>(byte_of(even, k), byte_of(odd, k), delta, lo);
+                    for (int k = 0; k < 4; ++k) v[k] = weight_pair<GT>(byte_of(even, k), byte_of(odd, k), delta, lo[slot]);
                 } else {
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
-                        const uint32_t c = code[(2 * p + (k >> 1)) % kCodeWords];
-                        v[k] = weight_pair<GT>(byte_of(c, 2 * (k & 1)), byte_of(c, 2 * (k & 1) + 1), delta, lo);
+                        const uint32_t c = code[slot][(2 * p + (k >> 1)) % kCodeWords];
+                        v[k] = weight_pair<GT>(byte_of(c, 2 * (k & 1)), byte_of(c, 2 * (k & 1) + 1), delta, lo[slot]);
                     }
                 }
-                ws[8 * c_row + ((4 * (tid & 1) + p) ^ tile_swizzle(c_row))] = v;
+                ws[8 * c_row + ((4 * (tid & 1) + p) ^ w_swizzle(c_row))] = v;
             }
         }
     };
@@ -249,21 +273,24 @@ __global__ __launch_bounds__(S::kThreads) void k_qsdp_tile(TileArgs a) {
     for (int i = 0; i < kN; ++i)
 #pragma unroll
         for (int j = 0; j < kM; ++j) acc[i][j] = (f32x4_v){0.0f, 0.0f, 0.0f, 0.0f};
-    const auto multiply = [&](int s) {
-        const u32x4_v *xs = x_at(s & 1), *ws = w_at(s & 1);
+    // piece 4 k + g of row n of a tile of 16; odd tiles of weights have another order
+    const int x_first = 8 * (wm + n), w_first = 8 * (wn + n);
+    int x_piece[2], w_piece[2][2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        x_piece[k] = x_first + ((4 * k + g) ^ x_swizzle(n));
+#pragma unroll
+        for (int i = 0; i < 2; ++i) w_piece[k][i] = w_first + ((4 * k + g) ^ w_swizzle(n + 16 * i));
+    }
+    const auto multiply = [&](int buffer) {
+        const u32x4_v *xs = x_at(buffer), *ws = w_at(buffer);
 #pragma unroll
         for (int k = 0; k < kTileDepth / 32; ++k) {
             u32x4_v wf[kN], xf[kM];
 #pragma unroll
-            for (int i = 0; i < kN; ++i) {
-                const int r = wn + 16 * i + n;
-                wf[i] = ws[8 * r + ((4 * k + g) ^ tile_swizzle(r))];
-            }
+            for (int i = 0; i < kN; ++i) wf[i] = ws[w_piece[k][i & 1] + 128 * i];
 #pragma unroll
-            for (int j = 0; j < kM; ++j) {
-                const int r = wm + 16 * j + n;
-                xf[j] = xs[8 * r + ((4 * k + g) ^ tile_swizzle(r))];
-            }
+            for (int j = 0; j < kM; ++j) xf[j] = xs[x_piece[k] + 128 * j];
 #pragma unroll
             for (int j = 0; j < kM; ++j)
 #pragma unroll
@@ -271,48 +298,77 @@ __global__ __launch_bounds__(S::kThreads) void k_qsdp_tile(TileArgs a) {
         }
     };
 
-    // ---- the pipeline
-    load_scales(begin);
+    // ---- the pipeline.  Step begin + i goes through slot i % kA and buffer i % 2.
+    static_assert(kA <= 2, "steps of the loop's body");
     if (GRAD) {
-        keep_table(begin & 1);
-        load_scales(begin + 1);
+        load_scales(begin, 0);
+        keep_table(0, 0);
+        load_scales(begin + 1, 0);
         __syncthreads();
     }
-    load(begin);
-    store(begin);
+    load(begin, 0);
+    store(0, 0);
     if (GRAD) {
-        keep_table((begin + 1) & 1);
-        load_scales(begin + 2);
-    } else if (begin + 1 < end) {
-        load_scales(begin + 1);
+        keep_table(1, 0);
+#pragma unroll
+        for (int i = 0; i < kA; ++i) load_scales(begin + 2 + i, i);
     }
-    if (begin + 1 < end) load(begin + 1);
+#pragma unroll
+    for (int i = 0; i < kA; ++i) load(begin + 1 + i, (1 + i) % kA);
     __syncthreads();
-    const auto advance = [&](int s) {
-        if (s + 1 < end) {
-            store(s + 1);
-            if (GRAD) {
-                keep_table(s & 1);
-                load_scales(s + 3);
-            }
-            if (s + 2 < end) {
-                if (!GRAD) load_scales(s + 2);
-                load(s + 2);
-            }
+    // the step after s (= begin + u, for what u decides) into LDS, another one on its way
+    const auto advance = [&](int s, int u) {
+        store((u + 1) & 1, (u + 1) % kA);
+        if (GRAD) {
+            keep_table(u & 1, u % kA);
+            load_scales(s + 2 + kA, u % kA);
         }
+        load(s + 1 + kA, (u + 1) % kA);
     };
-    if (wave < S::kWaves / 2) {
-        for (int s = begin; s < end; ++s) {
-            multiply(s);
-            advance(s);
-            __syncthreads();
+    if (S::kGroups > 1 ? !(group & 1) : wave < S::kWaves / 2) {
+        for (int i = 0; i < each; i += 2) {
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                if (i + u >= each) break;
+                if (begin + i + u < end) multiply(u);
+                advance(begin + i + u, u);
+                __syncthreads();
+            }
         }
     } else {
-        for (int s = begin; s < end; ++s) {
-            advance(s);
-            multiply(s);
-            __syncthreads();
+        for (int i = 0; i < each; i += 2) {
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                if (i + u >= each) break;
+                advance(begin + i + u, u);
+                if (begin + i + u < end) multiply(u);
+                __syncthreads();
+            }
         }
+    }
+
+    // ---- the groups' sums, in their order
+    if (S::kGroups > 1) {
+        f32x4_v *s_sum = reinterpret_cast<f32x4_v *>(s_all);
+        if (group > 0) {
+#pragma unroll
+            for (int i = 0; i < kN; ++i)
+#pragma unroll
+                for (int j = 0; j < kM; ++j)
+                    s_sum[(((group - 1) * S::kWaves + wave) * S::kFrags + i * kM + j) * 64 + lane] = acc[i][j];
+        }
+        __syncthreads();
+        if (group > 0) return;
+#pragma unroll
+        for (int k = 0; k < S::kGroups - 1; ++k)
+#pragma unroll
+            for (int i = 0; i < kN; ++i)
+#pragma unroll
+                for (int j = 0; j < kM; ++j) {
+                    const f32x4_v v = s_sum[((k * S::kWaves + wave) * S::kFrags + i * kM + j) * 64 + lane];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) acc[i][j][e] += v[e];
+                }
     }
 
     // ---- results
@@ -322,7 +378,8 @@ __global__ __launch_bounds__(S::kThreads) void k_qsdp_tile(TileArgs a) {
 #pragma unroll
         for (int i = 0; i < kN; ++i)
 #pragma unroll
-            for (int j = 0; j < kM; ++j) p[(i * kM + j) * 64] = acc[i][j];
+            for (int j = 0; j < kM; ++j)
+                if (t0 + wm + 16 * j < a.l.tokens) p[(i * kM + j) * 64] = acc[i][j];
         return;
     }
 #pragma unroll
