@@ -25,39 +25,77 @@ static void launch_rows_tiles(const LinearArgs &a, hipStream_t s) {
             a.cols >= 32 * kRowsChunk ? launch_rows<GT, BITS, GROUPS, 1, 1, 1, 8>(a, s) : launch_rows<GT, BITS, GROUPS, 1, 1, 2, 4>(a, s);
     } else if (a.tokens <= 32) {
         wide ? launch_rows<GT, BITS, GROUPS, 2, 2, 4, 2>(a, s) : launch_rows<GT, BITS, GROUPS, 1, 2, 2, 4>(a, s);
-    } else {
-        wide ? launch_rows<GT, BITS, GROUPS, 2, 4, 4, 2>(a, s) : launch_rows<GT, BITS, GROUPS, 1, 4, 4, 2>(a, s);
+    } else if constexpr (GROUPS == 1) {
+        launch_rows<GT, BITS, GROUPS, 2, 4, 4, 2>(a, s);
     }
 }
+// Whether every step of a row has one bucket.
+static bool whole_steps(const LinearArgs &a) { return a.cols % kRowsChunk == 0 && a.bucket % kRowsChunk == 0; }
+
+// Few tokens go to the streaming kernel: 32 over 28672 x 8192 52 us against the tiles' 84, over 20000 x 2048 16
+// against 24, over 4096 x 4096 15 each (4 bits; with buckets that change within a step the tiles come
+// as near as 37 to 39 us over 50257 x 1600).  Up to 64 only where a step has one bucket and the
+// matrix is large: 28672 x 8192 68 us against 88, but 20000 x 2048 25 each.
+static bool few_tokens(const LinearArgs &a) {
+    return a.tokens <= QSDP_LINEAR_EXACT_TOKENS ||
+           (a.tokens <= 64 && whole_steps(a) && a.rows * a.cols >= int64_t{1} << 26);
+}
+
 template <int GT, int BITS>
 static void launch_rows_groups(const LinearArgs &a, hipStream_t s) {
-    if (a.cols % kRowsChunk == 0 && a.bucket % kRowsChunk == 0)
+    if (whole_steps(a))
         launch_rows_tiles<GT, BITS, 1>(a, s);
     else
         launch_rows_tiles<GT, BITS, 4>(a, s);
 }
 
-using BigTile = TileShape<256, 256, 128, 64, 1, 1>;
-using SmallTile = TileShape<128, 128, 64, 64, 2, 2>;
+// Tiles, from the one that does most work a byte of LDS to the one that leaves fewest compute units
+// idle.
+using Tile0 = TileShape<256, 256, 128, 64, 1, 1>;
+using Tile1 = TileShape<128, 128, 64, 64, 2, 2>;
+using Tile2 = TileShape<64, 128, 32, 64, 2, 2>;
+using Tile3 = TileShape<64, 64, 32, 64, 4, 2>;
 
 // How a product is cut up: its tiles and how many workgroups share the depth of each.
 struct TilePlan {
-    bool big;
+    int shape;
     int64_t tiles_m, tiles_n;
     int splits;
-    size_t bytes;  // of partial results
 };
-static TilePlan tile_plan(int64_t tokens, int64_t width, int64_t depth) {
-    TilePlan p;
-    const int64_t big = ((tokens + 255) / 256) * ((width + 255) / 256);
-    p.big = big >= 192;
-    const int64_t side = p.big ? 256 : 128, room = 256, steps = (depth + kTileDepth - 1) / kTileDepth;
-    p.tiles_m = (tokens + side - 1) / side;
-    p.tiles_n = (width + side - 1) / side;
-    const int64_t tiles = p.tiles_m * p.tiles_n;
-    p.splits = (int)std::max<int64_t>(1, std::min({room / tiles, steps / 4, (int64_t)64}));
-    p.bytes = p.splits > 1 ? (size_t)tiles * p.splits * side * side * sizeof(float) : 0;
-    return p;
+
+constexpr int kMostSplits = 16;
+constexpr int64_t kPartialBytes = int64_t{1} << 26;  // of partial results at most
+
+// The cheapest by this estimate (us): a workgroup is alone on its compute unit, so there are as many rounds of
+// workgroups as 256 go into them, of so many steps each.  What a step takes was measured with 4-bit
+// codes, linear / gradient: first shape 2.4 (2048 x 16384 x 4096: 300 us in 2 x 64 steps) / 2.4 (500 x
+// 1600 x 50257, 16 workgroups a tile: 144 in 50), second 1.55 (1000 x 4096 x 4096: 53 in 32) / 1.9 (4096
+// x 1600 x 6400: 193 in 2 x 50), third 1.25 (333 x 4800 x 1600: 19 in 13) / 1.4 (512 x 4096 x 4096: 48
+// in 32), fourth 1.6 / 1.8 (the same: 63 in 2 x 16).  Sharing a tile's depth costs a second launch and
+// the partial results' way to memory and back: 2.5 us and 3 us for every 8 MB.
+static TilePlan tile_plan(int64_t tokens, int64_t width, int64_t depth, bool grad) {
+    static const struct {
+        int tm, tn, groups;
+        float step[2];
+    } shapes[4] = {{256, 256, 1, {2.4f, 2.4f}}, {128, 128, 2, {1.55f, 1.9f}}, {64, 128, 2, {1.25f, 1.4f}}, {64, 64, 4, {1.6f, 1.8f}}};
+    const int64_t steps = (depth + kTileDepth - 1) / kTileDepth;
+    TilePlan best{};
+    float least = 0.0f;
+    for (int i = 0; i < 4; ++i) {
+        const int64_t m = (tokens + shapes[i].tm - 1) / shapes[i].tm, n = (width + shapes[i].tn - 1) / shapes[i].tn;
+        for (int s = 1; s <= kMostSplits && s <= steps; s = s < 4 ? s + 1 : s < 8 ? s + 2 : s + 4) {
+            if (s > 1 && m * n * s * shapes[i].tm * shapes[i].tn * 4 > kPartialBytes) break;
+            const int64_t rounds = (m * n * s + 255) / 256;
+            const int64_t each = ((steps + s - 1) / s + shapes[i].groups - 1) / shapes[i].groups;
+            const float cost = (float)(rounds * each) * shapes[i].step[grad] +
+                               (s > 1 ? 2.5f + (float)(s * tokens * width) * (4.0f * 3.0f / 8e6f) : 0.0f);
+            if (least == 0.0f || cost < least) {
+                least = cost;
+                best = {i, m, n, s};
+            }
+        }
+    }
+    return best;
 }
 
 template <int GT, int BITS, bool GRAD, class S>
@@ -71,18 +109,23 @@ static void launch_tile(const TileArgs &a, hipStream_t s) {
 
 template <int GT, int BITS, bool GRAD>
 static void launch(const LinearArgs &l, hipStream_t s) {
-    if (!GRAD && l.tokens <= QSDP_LINEAR_EXACT_TOKENS) return launch_rows_groups<GT, BITS>(l, s);
+    if (!GRAD && few_tokens(l)) return launch_rows_groups<GT, BITS>(l, s);
     TileArgs a{};
     a.l = l;
     a.depth = GRAD ? l.rows : l.cols;
     a.width = GRAD ? l.cols : l.rows;
-    const TilePlan p = tile_plan(l.tokens, a.width, a.depth);
+    const TilePlan p = tile_plan(l.tokens, a.width, a.depth, GRAD);
     a.tiles_m = (int32_t)p.tiles_m;
     a.tiles_n = (int32_t)p.tiles_n;
     a.splits = p.splits;
     a.steps = (int32_t)((a.depth + kTileDepth - 1) / kTileDepth);
     a.partial = static_cast<float *>(l.workspace);
-    p.big ? launch_tile<GT, BITS, GRAD, BigTile>(a, s) : launch_tile<GT, BITS, GRAD, SmallTile>(a, s);
+    switch (p.shape) {
+        case 0: return launch_tile<GT, BITS, GRAD, Tile0>(a, s);
+        case 1: return launch_tile<GT, BITS, GRAD, Tile1>(a, s);
+        case 2: return launch_tile<GT, BITS, GRAD, Tile2>(a, s);
+        default: return launch_tile<GT, BITS, GRAD, Tile3>(a, s);
+    }
 }
 template <bool GRAD>
 static void dispatch(onebit_dtype_t dtype, int bits, const LinearArgs &a, hipStream_t s) {
@@ -97,9 +140,9 @@ constexpr int64_t kLinearMost = 1 << 24;  // tokens, rows and columns are below
 static size_t linear_workspace(int64_t tokens, int64_t rows, int64_t cols) {
     if (tokens < 0 || tokens >= kLinearMost || rows < 1 || rows >= kLinearMost || cols < 32 || cols >= kLinearMost || cols % 32)
         return 0;
-    if (tokens == 0) return 16;
-    const size_t linear = tokens > QSDP_LINEAR_EXACT_TOKENS ? tile_plan(tokens, rows, cols).bytes : 0;
-    return std::max({(size_t)16, linear, tile_plan(tokens, cols, rows).bytes});
+    // the most that tile_plan may share out, whatever it takes
+    const int64_t m = (tokens + 255) / 256 * 256, n = (std::max(rows, cols) + 255) / 256 * 256;
+    return (size_t)std::max<int64_t>(16, std::min(kPartialBytes, m * n * 4 * kMostSplits));
 }
 
 template <bool GRAD>

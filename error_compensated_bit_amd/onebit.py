@@ -74,7 +74,7 @@ _SIGS = {
 }
 
 QSDP_STATS_PARTIALS = 1024
-QSDP_LINEAR_EXACT_TOKENS = 64
+QSDP_LINEAR_EXACT_TOKENS = 32
 
 _lib = None
 

@@ -450,7 +450,7 @@ typedef struct {
  * holds before a call does not matter.  Calls that may overlap in time need one each, and
  * so do two captured graphs that may be replayed at the same time.  (0 is returned for
  * sizes that the calls refuse.)  The calls are not among the classes of the launch timing above. */
-#define QSDP_LINEAR_EXACT_TOKENS 64
+#define QSDP_LINEAR_EXACT_TOKENS 32
 size_t qsdp_linear_workspace_bytes(int64_t tokens, int64_t rows, int64_t cols);
 onebit_status_t qsdp_linear(const void *x, onebit_dtype_t dtype, int64_t tokens, int64_t x_stride,
                             const qsdp_matrix_t *w, void *out, int64_t out_stride, void *workspace,

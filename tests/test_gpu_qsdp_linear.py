@@ -69,7 +69,7 @@ def padded(x):
     return y[:, :n]
 
 
-TOKENS = [1, 2, 15, 16, 17, 33, 48, 63, 64, 65, 100, 129, 300]
+TOKENS = [1, 2, 15, 16, 17, 32, 33, 48, 63, 64, 65, 100, 129, 300]
 # (rows, cols, bucket): single rows, odd counts, buckets inside, across and over many rows
 SHAPES = [(1, 32, 32), (17, 32, 1024), (40, 64, 32), (127, 160, 1024), (200, 96, 96), (65, 416, 64), (33, 1600, 1024),
           (300, 128, 128), (129, 1024, 256), (50, 2080, 2080), (260, 544, 1088), (16, 4096, 65536)]
@@ -97,7 +97,7 @@ def test_whole_numbers_come_out_to_the_bit(op, bits, rows, cols, bucket, dtype):
 @pytest.mark.parametrize("rows,cols,bucket", SHAPES + [(6400, 1600, 1024), (515, 8192, 128), (5003, 64, 32)])
 @pytest.mark.parametrize("dtype", [BF16, F16])
 def test_products_within_the_counted_roundings(op, bits, rows, cols, bucket, dtype):
-    for tokens in (1, 3, 16, 31, 64, 65, 200, 515):
+    for tokens in (1, 3, 16, 32, 33, 64, 65, 200, 515):
         g = gen("product", op, rows, cols, tokens)
         weights = coded(rows, cols, bucket, bits, g)
         x = torch.randn(tokens, cols if op == "linear" else rows, generator=g)
@@ -124,6 +124,19 @@ def test_many_tokens(op, rows, cols, bits, bucket, dtype):
     x = torch.randn(tokens, depth, generator=g).to(dtype)
     want, tol = expect(op, x.to(DEV), weights, rows, cols, bucket, bits)
     assert torch.all((run(op, padded(x), dev(weights), rows, cols, bucket, bits).double() - want).abs() <= tol)
+
+
+@pytest.mark.parametrize("bits,bucket", [(4, 128), (8, 1024)])
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("rows,cols", [(16500, 256), (16411, 4224)])
+def test_large_matrices(rows, cols, bits, bucket, dtype):
+    """Up to 64 tokens over matrices of enough rows and columns for the widest streams."""
+    g = gen("large", rows, bits)
+    weights = dev(coded(rows, cols, bucket, bits, g, whole=True))
+    for tokens in (1, 16, 17, 32, 33, 50, 64, 65):
+        x = torch.randint(-2, 3, (tokens, cols), generator=g).to(dtype)
+        want = expect("linear", x.to(DEV), weights, rows, cols, bucket, bits)[0].float().to(dtype)
+        assert torch.equal(run("linear", padded(x), weights, rows, cols, bucket, bits), want), tokens
 
 
 @pytest.mark.parametrize("tokens", [5, 40, 130])
