@@ -4,8 +4,8 @@
 // A workgroup has TM x TN results and goes through the depth in steps of 64.  A step's x
 // and its weights, expanded once for all TM rows and rounded to x's type, lie in LDS twice over:
 // while one is multiplied the next is written and the one after that is on its way from memory.
-// Half of the waves write first and multiply then, the others the other way round, so that of
-// two waves on a SIMD one keeps the matrix cores busy while the other expands.
+// Each wave writes first and multiplies then: of two waves on a SIMD one comes to its products
+// while the other still expands (half of them the other way round: twice the code, and no faster).
 //
 // LDS: rows of 64 values (128 bytes) of x and of weights, the 16-byte pieces of row r in the order
 // p ^ x_swizzle(r) or p ^ w_swizzle(r), so that what eight lanes read or write at once lies in
@@ -174,13 +174,16 @@ __global__ __launch_bounds__(S::kThreads * S::kGroups, S::kOccupancy) void k_qsd
             for (int m = 0; m < S::kXPieces; ++m)
                 xr[slot][m] = *reinterpret_cast<const u32x4_v *>(x + 2 * d0 + x_off[m]);
         } else {
-            // the depth's end: value by value, zeros behind it
+            // the depth's end: value by value, the last one and zeros for those behind it
+            const int left = (int)(a.depth - d0) - 8 * (tid & 7);
 #pragma unroll
             for (int m = 0; m < S::kXPieces; ++m) {
                 const uint16_t *p = reinterpret_cast<const uint16_t *>(x + 2 * d0 + x_off[m]);
                 uint32_t v[8];
 #pragma unroll
-                for (int k = 0; k < 8; ++k) v[k] = d0 + 8 * (tid & 7) + k < a.depth ? p[k] : 0u;
+                for (int k = 0; k < 8; ++k) v[k] = p[min(k, left - 1)];
+#pragma unroll
+                for (int k = 0; k < 8; ++k) v[k] = k < left ? v[k] : 0u;
                 xr[slot][m] = (u32x4_v){v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16, v[6] | v[7] << 16};
             }
         }
@@ -228,21 +231,23 @@ __global__ __launch_bounds__(S::kThreads * S::kGroups, S::kOccupancy) void k_qsd
 #pragma unroll
         for (int m = 0; m < S::kXPieces; ++m) xs[S::kThreads * m] = xr[slot][m];
         if (GRAD) {
-            float2 e[8];
+            // the minima and steps of two rows at a time, for all four columns
+            const float2 *e = table_at(buffer) + c_row * (S::TN / 32) + (c_col >> 5);
+            u32x4_v v[4];
 #pragma unroll
-            for (int r = 0; r < 8; ++r) e[r] = table_at(buffer)[(c_row + r) * (S::TN / 32) + (c_col >> 5)];
+            for (int p = 0; p < 4; ++p) {
+                const float2 e0 = e[2 * p * (S::TN / 32)], e1 = e[(2 * p + 1) * (S::TN / 32)];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const uint32_t c0 = code[slot][2 * p] >> (BITS * k), c1 = code[slot][2 * p + 1] >> (BITS * k);
+                    constexpr uint32_t m = (1u << BITS) - 1;
+                    v[k][p] = round_pair<GT>(__fmaf_rn((float)(c0 & m), e0.y, e0.x), __fmaf_rn((float)(c1 & m), e1.y, e1.x));
+                }
+            }
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 const int o = c_col + k;
-                float w[8];
-#pragma unroll
-                for (int r = 0; r < 8; ++r) {
-                    const uint32_t c = code[slot][r];
-                    w[r] = __fmaf_rn((float)(BITS == 4 ? (c >> (4 * k)) & 15u : (c >> (8 * k)) & 255u), e[r].y, e[r].x);
-                }
-                ws[8 * o + ((c_row >> 3) ^ w_swizzle(o))] =
-                    (u32x4_v){round_pair<GT>(w[0], w[1]), round_pair<GT>(w[2], w[3]), round_pair<GT>(w[4], w[5]),
-                              round_pair<GT>(w[6], w[7])};
+                ws[8 * o + ((c_row >> 3) ^ w_swizzle(o))] = v[k];
             }
         } else {
             const float delta = bucket_delta<BITS>(lo[slot], hi[slot]);
@@ -292,9 +297,9 @@ __global__ __launch_bounds__(S::kThreads * S::kGroups, S::kOccupancy) void k_qsd
 #pragma unroll
             for (int j = 0; j < kM; ++j) xf[j] = xs[x_piece[k] + 128 * j];
 #pragma unroll
-            for (int j = 0; j < kM; ++j)
+            for (int i = 0; i < kN; ++i)
 #pragma unroll
-                for (int i = 0; i < kN; ++i) acc[i][j] = product16<GT>(wf[i], xf[j], acc[i][j]);
+                for (int j = 0; j < kM; ++j) acc[i][j] = product16<GT>(wf[i], xf[j], acc[i][j]);
         }
     };
 
@@ -325,25 +330,15 @@ __global__ __launch_bounds__(S::kThreads * S::kGroups, S::kOccupancy) void k_qsd
         }
         load(s + 1 + kA, (u + 1) % kA);
     };
-    if (S::kGroups > 1 ? !(group & 1) : wave < S::kWaves / 2) {
-        for (int i = 0; i < each; i += 2) {
+    for (int i = 0; i < each; i += 2) {
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                if (i + u >= each) break;
-                if (begin + i + u < end) multiply(u);
-                advance(begin + i + u, u);
-                __syncthreads();
-            }
-        }
-    } else {
-        for (int i = 0; i < each; i += 2) {
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                if (i + u >= each) break;
-                advance(begin + i + u, u);
-                if (begin + i + u < end) multiply(u);
-                __syncthreads();
-            }
+        for (int u = 0; u < 2; ++u) {
+            if (i + u >= each) break;
+            advance(begin + i + u, u);
+            // (The condition holds without groups, but without the branch the compiler mixes the linear
+            // product's expansion into its products: 305 us for 289.  The gradient gains by it, 130 for 135.)
+            if ((GRAD && S::kGroups == 1) || begin + i + u < end) multiply(u);
+            __syncthreads();
         }
     }
 
