@@ -296,10 +296,12 @@ __global__ __launch_bounds__(S::kThreads * S::kGroups, S::kOccupancy) void k_qsd
             for (int i = 0; i < kN; ++i) wf[i] = ws[w_piece[k][i & 1] + 128 * i];
 #pragma unroll
             for (int j = 0; j < kM; ++j) xf[j] = xs[x_piece[k] + 128 * j];
+            // (the order that leaves the compiler the better schedule: 285 against 289 us, 130 against 145)
 #pragma unroll
-            for (int i = 0; i < kN; ++i)
-#pragma unroll
-                for (int j = 0; j < kM; ++j) acc[i][j] = product16<GT>(wf[i], xf[j], acc[i][j]);
+            for (int q = 0; q < kN * kM; ++q) {
+                const int i = GRAD ? q % kN : q / kM, j = GRAD ? q / kN : q % kM;
+                acc[i][j] = product16<GT>(wf[i], xf[j], acc[i][j]);
+            }
         }
     };
 
