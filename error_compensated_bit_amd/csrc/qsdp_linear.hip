@@ -64,7 +64,13 @@ struct TilePlan {
 };
 
 constexpr int kMostSplits = 16;
-constexpr int64_t kPartialBytes = int64_t{1} << 26;  // of partial results at most
+
+// Bytes of partial results at most: as many parts of the result, in whole tiles, but not more than 64 MB.
+static int64_t partial_room(int64_t tokens, int64_t width) {
+    const int64_t m = tokens > 128 ? (tokens + 255) / 256 * 256 : (tokens + 63) / 64 * 64;
+    const int64_t n = width > 256 ? (width + 255) / 256 * 256 : (width + 127) / 128 * 128;
+    return std::min(m * n * 4 * kMostSplits, int64_t{1} << 26);
+}
 
 // The cheapest by this estimate (us): a workgroup is alone on its compute unit, so there are as many rounds of
 // workgroups as 256 go into them, of so many steps each.  What a step takes was measured with 4-bit
@@ -79,12 +85,13 @@ static TilePlan tile_plan(int64_t tokens, int64_t width, int64_t depth, bool gra
         float step[2];
     } shapes[4] = {{256, 256, 1, {2.4f, 2.4f}}, {128, 128, 2, {1.55f, 1.9f}}, {64, 128, 2, {1.25f, 1.4f}}, {64, 64, 4, {1.6f, 1.8f}}};
     const int64_t steps = (depth + kTileDepth - 1) / kTileDepth;
+    const int64_t room = partial_room(tokens, width);
     TilePlan best{};
     float least = 0.0f;
     for (int i = 0; i < 4; ++i) {
         const int64_t m = (tokens + shapes[i].tm - 1) / shapes[i].tm, n = (width + shapes[i].tn - 1) / shapes[i].tn;
         for (int s = 1; s <= kMostSplits && s <= steps; s = s < 4 ? s + 1 : s < 8 ? s + 2 : s + 4) {
-            if (s > 1 && m * n * s * shapes[i].tm * shapes[i].tn * 4 > kPartialBytes) break;
+            if (s > 1 && m * n * s * shapes[i].tm * shapes[i].tn * 4 > room) break;
             const int64_t rounds = (m * n * s + 255) / 256;
             const int64_t each = ((steps + s - 1) / s + shapes[i].groups - 1) / shapes[i].groups;
             const float cost = (float)(rounds * each) * shapes[i].step[grad] +
@@ -140,9 +147,7 @@ constexpr int64_t kLinearMost = 1 << 24;  // tokens, rows and columns are below
 static size_t linear_workspace(int64_t tokens, int64_t rows, int64_t cols) {
     if (tokens < 0 || tokens >= kLinearMost || rows < 1 || rows >= kLinearMost || cols < 32 || cols >= kLinearMost || cols % 32)
         return 0;
-    // the most that tile_plan may share out, whatever it takes
-    const int64_t m = (tokens + 255) / 256 * 256, n = (std::max(rows, cols) + 255) / 256 * 256;
-    return (size_t)std::max<int64_t>(16, std::min(kPartialBytes, m * n * 4 * kMostSplits));
+    return (size_t)std::max(partial_room(tokens, std::max(rows, cols)), int64_t{16});
 }
 
 template <bool GRAD>

@@ -109,7 +109,7 @@ __global__ __launch_bounds__(S::kThreads * S::kGroups, S::kOccupancy) void k_qsd
     const uint32_t row_bytes = row_parts * (4 * BITS);
     constexpr int kCodeWords = GRAD ? 8 : BITS;  // columns of eight rows, or words of 32 codes
     uint32_t code[kA][kCodeWords];
-    float lo[kA], hi[kA];
+    float lo[kA + 2], hi[kA + 2];  // (two more for the gradient's first tables)
     // linear: this thread's row and half of a step.  gradient: rows 8 (tid / (TN / 4)) + 0 .. 7 of a step, columns
     // 4 (tid % (TN / 4)) + 0 .. 3, and an entry of the step's table of minima and steps: row tid / (TN / 32),
     // columns 32 (tid % (TN / 32)) + 0 .. 31.
@@ -307,21 +307,22 @@ __global__ __launch_bounds__(S::kThreads * S::kGroups, S::kOccupancy) void k_qsd
 
     // ---- the pipeline.  Step begin + i goes through slot i % kA and buffer i % 2.
     static_assert(kA <= 2, "steps of the loop's body");
+    // Everything is asked for before the first wait.
     if (GRAD) {
-        load_scales(begin, 0);
-        keep_table(0, 0);
-        load_scales(begin + 1, 0);
-        __syncthreads();
+        load_scales(begin, kA);
+        load_scales(begin + 1, kA + 1);
     }
-    load(begin, 0);
-    store(0, 0);
+#pragma unroll
+    for (int i = 0; i < kA; ++i) load(begin + i, i);
     if (GRAD) {
-        keep_table(1, 0);
 #pragma unroll
         for (int i = 0; i < kA; ++i) load_scales(begin + 2 + i, i);
+        keep_table(0, kA);
+        keep_table(1, kA + 1);
+        __syncthreads();
     }
-#pragma unroll
-    for (int i = 0; i < kA; ++i) load(begin + 1 + i, (1 + i) % kA);
+    store(0, 0);
+    load(begin + kA, 0);
     __syncthreads();
     // the step after s (= begin + u, for what u decides) into LDS, another one on its way
     const auto advance = [&](int s, int u) {
@@ -400,12 +401,19 @@ __global__ __launch_bounds__(256) void k_qsdp_tile_join(TileArgs a) {
     if (t >= a.l.tokens || o >= a.width) return;
     const f32x4_v *p = reinterpret_cast<const f32x4_v *>(a.partial) +
                        ((tile * a.splits * S::kWaves + wave) * S::kFrags + frag) * 64 + lane;
+    constexpr int64_t kStep = S::kWaves * S::kFrags * 64;
     f32x4_v v = *p;
-    for (int s = 1; s < a.splits; ++s) {
-        p += S::kWaves * S::kFrags * 64;
-        const f32x4_v q = *p;
+    // four parts at a time, so that a wait is for four (behind the last one: the last one, not used)
+    for (int s = 1; s < a.splits; s += 4) {
+        f32x4_v q[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] += q[e];
+        for (int k = 0; k < 4; ++k) q[k] = p[min(s + k, a.splits - 1) * kStep];
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (s + k < a.splits) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) v[e] += q[k][e];
+            }
     }
     store_results<GT>(a, t, o, v);
 }
