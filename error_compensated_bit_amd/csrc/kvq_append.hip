@@ -9,6 +9,9 @@
 // written once.  A lane holds eight consecutive values of a head, as in kvq_quantize; it takes
 // the same place of kAppendHeads heads, so that the cosines and sines, four times a row's
 // bytes, are read once for them.
+//
+// Measured: 16384 tokens of 32 + 2 x 8 heads of 128, bf16, 4 bits, 83 to 90 us for 362 MB (4.0 to 4.4 TB/s;
+// a copy moves 4.8); 5003 of 16 + 2 x 16 heads of 64, fp16, 8 bits, 13.6 us; 64 tokens 5.3 us.
 #include "kvq_rows.h"
 
 namespace onebit {

@@ -13,6 +13,11 @@
 // which LDS turns into the operands' order.  The waves of a group share the columns and with
 // them x, which goes through LDS too; groups share the columns of the same rows among them and
 // add up in LDS at the end.
+//
+// Measured (a copy moves 4.8 TB/s): 32 tokens over 28672 x 8192, 4 bits, 50 us for 134 MB (2.7 TB/s);
+// 5 over 50257 x 1600, 8 bits, buckets of 1024, 25 to 28 us for 82 MB; one over 6400 x 1600, 4 bits, 6.7
+// us, of which a launch is 4.  Without its products the first takes 40, the second 26: what the loop
+// reads, 128 bytes of eight rows at a time, comes at 3.3 to 4 TB/s (alone, in a probe, 5).
 #pragma once
 
 #include "qsdp_linear.h"

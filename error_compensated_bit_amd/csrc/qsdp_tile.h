@@ -12,6 +12,11 @@
 // different banks, while rows a multiple of 32 apart (of 16, for x) have one order: their
 // addresses differ by a constant.  An operand of v_mfma_f32_16x16x32 is one piece of 16 rows.  Weights are the first
 // operand, so that a lane holds four neighbouring results of one row of x.
+//
+// Measured: 2048 x 16384 x 4096, 4 bits, bf16, 278 to 290 us (0.95 to 0.99 PFLOP/s; the library's product
+// with decoded weights, 200); gradient of 4096 x 1600 x 6400 129 us (97), of 500 x 1600 x 50257, fp16,
+// 8 bits, 130 us (269).  Small products are bound by a step's chain of waits, 1.2 us: 333 x 4800 x
+// 1600 17 us, 77 x 4096 x 4096 19.
 #pragma once
 
 #include "qsdp_linear.h"

@@ -586,7 +586,7 @@ def kvq_quantize(k, v, slots, k_codes, k_scales, v_codes, v_scales, *, bits, str
     kt, kh = _kvq_rows(k, cache.kv_heads, cache.head_dim, "k")
     vt, vh = _kvq_rows(v, cache.kv_heads, cache.head_dim, "v")
     _call("kvq_quantize", device, stream, k.data_ptr(), v.data_ptr(), _dtype_code(k), k.shape[0], kt, kh, vt, vh,
-              _kvq_slots(slots, k.shape[0]), C.byref(cache))
+          _kvq_slots(slots, k.shape[0]), C.byref(cache))
 
 
 def kvq_append(q, k, v, positions, rotary, slots, k_codes, k_scales, v_codes, v_scales, q_out, *, bits, interleaved=False,
@@ -631,7 +631,7 @@ def kvq_dequantize(k_codes, k_scales, v_codes, v_scales, slots, k_out, v_out, *,
         raise ValueError("k_out and v_out must have one shape and type")
     _kvq_rows(k_out, cache.kv_heads, cache.head_dim, "k_out")
     _call("kvq_dequantize", device, stream, C.byref(cache), _kvq_slots(slots, k_out.shape[0]), k_out.shape[0],
-              _dense(k_out, k_out.dtype, "k_out"), _dense(v_out, v_out.dtype, "v_out"), _dtype_code(k_out))
+          _dense(k_out, k_out.dtype, "k_out"), _dense(v_out, v_out.dtype, "v_out"), _dtype_code(k_out))
 
 
 def kvq_attention_workspace_bytes(batch, total_q, q_heads, kv_heads, head_dim) -> int:
@@ -669,9 +669,9 @@ def kvq_attention(q, k_codes, k_scales, v_codes, v_scales, block_table, kv_lens,
     if abs(window) >= 2 ** 31:                 # (would be cut to 32 bits on its way)
         raise ValueError(f"window must be from 0 to 2^31 - 1, got {window}")
     _call("kvq_attention", device, stream, q.data_ptr(), _dtype_code(q), total, q_heads, qt, qh,
-              None if q_offsets is None else _dense(q_offsets, torch.int32, "q_offsets"),
-              _dense(kv_lens, torch.int32, "kv_lens"), batch, block_table.data_ptr(), max_pages,
-              block_table.stride(0) if batch > 1 else max_pages, C.byref(cache),
-              cache.head_dim ** -0.5 if scale is None else float(scale), float(softcap), int(window),
-              _dense(out, q.dtype, "out"), None if lse is None else _dense(lse, torch.float32, "lse"),
-              _ptr(workspace), workspace.numel() * workspace.element_size())
+          None if q_offsets is None else _dense(q_offsets, torch.int32, "q_offsets"),
+          _dense(kv_lens, torch.int32, "kv_lens"), batch, block_table.data_ptr(), max_pages,
+          block_table.stride(0) if batch > 1 else max_pages, C.byref(cache),
+          cache.head_dim ** -0.5 if scale is None else float(scale), float(softcap), int(window),
+          _dense(out, q.dtype, "out"), None if lse is None else _dense(lse, torch.float32, "lse"),
+          _ptr(workspace), workspace.numel() * workspace.element_size())

@@ -435,17 +435,20 @@ typedef struct {
  * The second is the gradient that the first hands back to its input; the weights' own is
  * the plain product of dy and x.  From one token (a decoding step) to a training batch.
  * x, dy: bf16 or fp16 (ONEBIT_ERR_UNSUPPORTED otherwise), row t at base + t * stride
- * elements, 16-byte aligned base, stride a multiple of 8 (ONEBIT_ERR_ALIGN otherwise) and
- * at least the row's length; what lies between two rows is never used.  out, dx: the same type,
- * any stride of at least the row's length, which leaves what lies between two rows as it was.
- * 0 <= tokens < 2^24; no tokens: the call does nothing.
+ * elements, 16-byte aligned base, stride a multiple of 8 (ONEBIT_ERR_ALIGN otherwise), at
+ * least the row's length and below 2^23; what lies between two rows is never used.  out, dx: the
+ * same type, any stride of at least the row's length and below 2^32; what lies between two
+ * rows stays as it was.  (A single row's stride is not looked at.)  0 <= tokens < 2^24; no tokens:
+ * the call does nothing.
  * Sums are binary32.  Roundings before them: none in qsdp_linear with up to
  * QSDP_LINEAR_EXACT_TOKENS tokens, where codes and minima enter apart; else of the weights
- * to the type of x or dy, nearest even (for fp16, weights above 65504 become infinite).
+ * to the type of x or dy, nearest even (for fp16, weights above 65504 become infinite).  A bucket
+ * has 2^bits weights, so equal codes' errors are equal: a result is off by half a step of the
+ * type times sum |x w| at most, and by less only as far as the signs of x differ.
  * A value of x or dy that is not finite leaves nothing finite in its own row of the result and
  * makes no difference to the others; a bucket whose minimum or maximum is not finite leaves
  * nothing finite in the results that use its weights, and makes no difference to the others.
- * (Sums of |x| over a row times 2^11 delta are to stay below 2^127.)
+ * (Sums of |x| over a row times 2^9 of its largest delta are to stay below 2^127.)
  * workspace: qsdp_linear_workspace_bytes bytes (for either call), 16-byte aligned; what it
  * holds before a call does not matter.  Calls that may overlap in time need one each, and
  * so do two captured graphs that may be replayed at the same time.  (0 is returned for

@@ -312,6 +312,66 @@ def test_captured_and_replayed(tokens):
         assert torch.equal(out, want[0]) and torch.equal(dx, want[1])
 
 
+def test_two_calls_at_once():
+    """Two streams with a workspace each, tiles whose depth is shared."""
+    rows, cols, bucket, bits, tokens = 500, 4096, 1024, 4, 90
+    g = gen("two")
+    weights = dev(coded(rows, cols, bucket, bits, g, whole=True))
+    xs = [torch.randint(-2, 3, (tokens, cols), generator=g).to(BF16) for _ in range(2)]
+    want = [expect("linear", x.to(DEV), weights, rows, cols, bucket, bits)[0].float().to(BF16) for x in xs]
+    xd = [padded(x) for x in xs]
+    ws = [torch.zeros(ob.qsdp_linear_workspace_bytes(tokens, rows, cols), dtype=torch.uint8, device=DEV) for _ in xs]
+    outs = [[torch.zeros(tokens, rows, dtype=BF16, device=DEV) for _ in range(8)] for _ in xs]
+    streams = [torch.cuda.Stream() for _ in xs]
+    torch.cuda.synchronize()
+    for i in range(8):
+        for k in range(2):
+            run("linear", xd[k], weights, rows, cols, bucket, bits, workspace=ws[k], out=outs[k][i], stream=streams[k])
+    torch.cuda.synchronize()
+    for k in range(2):
+        assert all(torch.equal(o, want[k]) for o in outs[k])
+
+
+@pytest.mark.parametrize("tokens", [2, 40])
+def test_codes_past_4_gib(tokens):
+    """A matrix of 5.4e9 weights, 5 GiB of codes: rows far apart, by single columns and single rows."""
+    rows, cols, bucket, bits = 1 << 20, 5120, 1024, 8
+    g = torch.Generator(device=DEV).manual_seed(3)
+    codes = torch.randint(0, 256, (rows * cols,), generator=g, dtype=torch.uint8, device=DEV)
+    lo = -torch.randint(100, 129, (rows * cols // bucket,), generator=g, device=DEV).float()
+    hi = lo + 255.0
+    look = torch.tensor([0, 1, 77777, 409600, 419430, 838860, 838861, rows - 2, rows - 1], device=DEV)
+    flat = look.unsqueeze(1) * cols + torch.arange(cols, device=DEV)
+    w = lo[flat // bucket] + codes[flat].float()                            # whole numbers up to 155
+    x = torch.zeros(tokens, cols, dtype=BF16, device=DEV)
+    x[0, 5], x[1, 5119], x[1, 7] = 1, 1, 1
+    ws = torch.zeros(ob.qsdp_linear_workspace_bytes(tokens, rows, cols), dtype=torch.uint8, device=DEV)
+    out = torch.zeros(tokens, rows, dtype=BF16, device=DEV)
+    ob.qsdp_linear(x, codes, lo, hi, out, bucket=bucket, bits=bits, workspace=ws)
+    assert torch.equal(out[:, look].float(), (x.float() @ w.t()).to(BF16).float())
+    dy = torch.zeros(tokens, rows, dtype=BF16, device=DEV)
+    for i, r in enumerate(look.tolist()):
+        dy[i % tokens, r] = 1
+    dx = torch.zeros(tokens, cols, dtype=BF16, device=DEV)
+    ob.qsdp_linear_grad(dy, codes, lo, hi, dx, bucket=bucket, bits=bits, workspace=ws)
+    assert torch.equal(dx.float(), (dy[:, look].float() @ w).to(BF16).float())
+
+
+def test_rows_of_the_input_far_apart():
+    """Strides near their limit: a tile's rows span more than 2 GiB."""
+    rows, cols, bucket, bits, tokens, stride = 96, 128, 128, 4, 260, (1 << 23) - 8
+    g = gen("far rows")
+    weights = dev(coded(rows, cols, bucket, bits, g, whole=True))
+    room = torch.empty(tokens * stride, dtype=BF16, device=DEV)
+    for op, a in (("linear", cols), ("grad", rows)):
+        x = torch.randint(-2, 3, (tokens, a), generator=g).to(BF16).to(DEV)
+        far = room.view(tokens, stride)[:, 16:16 + a]
+        far.copy_(x)
+        want = expect(op, x, weights, rows, cols, bucket, bits)[0].float().to(BF16)
+        assert torch.equal(run(op, far, weights, rows, cols, bucket, bits), want)
+        assert torch.equal(run(op, far[:20], weights, rows, cols, bucket, bits), want[:20])
+
+
 def test_bindings_refusals():
     rows, cols, bucket, bits = 96, 64, 128, 4
     weights = dev(coded(rows, cols, bucket, bits, gen("refuse")))

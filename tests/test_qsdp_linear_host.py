@@ -44,7 +44,7 @@ def test_bad_matrices_are_refused(name, fields, status):
     (dict(dtype=ob.ONEBIT_F32), UNSUP), (dict(dtype=3), INV), (dict(dtype=-1), INV), (dict(tokens=-1), INV),
     (dict(tokens=1 << 24), INV), (dict(x=None), INV), (dict(out=None), INV), (dict(ws=None), INV), (dict(ws_bytes=0), INV),
     (dict(xs=56), INV), (dict(os=63), INV), (dict(xs=0), INV), (dict(xs=-128), INV), (dict(os=-128), INV),
-    (dict(xs=1 << 32), INV), (dict(os=1 << 32), INV), (dict(xs=132), ALIGN), (dict(x=A + 8), ALIGN), (dict(out=A + 1), ALIGN),
+    (dict(xs=1 << 23), INV), (dict(os=1 << 32), INV), (dict(xs=132), ALIGN), (dict(x=A + 8), ALIGN), (dict(out=A + 1), ALIGN),
     (dict(ws=A + 8), ALIGN), (dict(tokens=0, x=None, out=None, ws=None), OK),
 ])
 def test_refusals(name, kw, status):
