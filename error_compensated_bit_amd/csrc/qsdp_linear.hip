@@ -15,35 +15,36 @@ static void launch_rows(const LinearArgs &a, hipStream_t s) {
     hipLaunchKernelGGL((k_qsdp_rows<GT, BITS, GROUPS, NT, MT, WAVES, SPLIT>), dim3((unsigned)((a.rows + each - 1) / each)),
                        dim3(64 * WAVES * SPLIT), 0, s, a);
 }
+// The fewest rows of the matrix for a workgroup that leave one workgroup to a compute unit, the rest of its
+// waves sharing the columns: 16, 32 or 64 (32 tokens, 4 bits: 8192 x 8192 38, 25, 32 us; 14336 x 4096 45,
+// 27, 19).  Eight groups need more than four loads of columns.  Up to 128 rows a unit, 128 for more than 16 tokens
+// (28672 x 8192 49 us against 64) and 64 otherwise (38 and 37); above, workgroups of a single group, of
+// which more are on a unit at a time (32 tokens, 50304 x 1600 38 us against 47, one token 24 against 29).
+template <int GT, int BITS, int GROUPS, int MT>
+static void launch_rows_split(const LinearArgs &a, hipStream_t s) {
+    const int64_t each = (a.rows + 255) / 256, loads = (a.cols * BITS + 8 * kRowsChunk - 1) / (8 * kRowsChunk);
+    if (each <= 16 && loads > 4) return launch_rows<GT, BITS, GROUPS, 1, MT, 1, 8>(a, s);
+    if (each <= 32) return launch_rows<GT, BITS, GROUPS, 1, MT, 2, 4>(a, s);
+    if (each <= 64 || (each <= 128 && MT == 1)) return launch_rows<GT, BITS, GROUPS, 1, MT, 4, 2>(a, s);
+    if constexpr (MT > 1)
+        if (each <= 128) return launch_rows<GT, BITS, GROUPS, 2, MT, 4, 2>(a, s);
+    launch_rows<GT, BITS, GROUPS, 1, MT, 4, 1>(a, s);
+}
 template <int GT, int BITS, int GROUPS>
 static void launch_rows_tiles(const LinearArgs &a, hipStream_t s) {
-    const bool wide = a.rows >= 64 * 256;
-    if (a.tokens <= 16) {
-        if (wide)
-            a.cols >= 32 * kRowsChunk ? launch_rows<GT, BITS, GROUPS, 1, 1, 4, 2>(a, s) : launch_rows<GT, BITS, GROUPS, 1, 1, 4, 1>(a, s);
-        else
-            a.cols >= 32 * kRowsChunk ? launch_rows<GT, BITS, GROUPS, 1, 1, 1, 8>(a, s) : launch_rows<GT, BITS, GROUPS, 1, 1, 2, 4>(a, s);
-    } else if (a.tokens <= 32) {
-        wide ? launch_rows<GT, BITS, GROUPS, 2, 2, 4, 2>(a, s) : launch_rows<GT, BITS, GROUPS, 1, 2, 2, 4>(a, s);
-    } else if constexpr (GROUPS == 1) {
-        launch_rows<GT, BITS, GROUPS, 2, 4, 4, 2>(a, s);
-    }
+    a.tokens <= 16 ? launch_rows_split<GT, BITS, GROUPS, 1>(a, s) : launch_rows_split<GT, BITS, GROUPS, 2>(a, s);
 }
-// Whether every step of a row has one bucket.
-static bool whole_steps(const LinearArgs &a) { return a.cols % kRowsChunk == 0 && a.bucket % kRowsChunk == 0; }
 
-// Few tokens go to the streaming kernel: 32 over 28672 x 8192 52 us against the tiles' 84, over 20000 x 2048 16
-// against 24, over 4096 x 4096 15 each (4 bits; with buckets that change within a step the tiles come
-// as near as 37 to 39 us over 50257 x 1600).  Up to 64 only where a step has one bucket and the
-// matrix is large: 28672 x 8192 68 us against 88, but 20000 x 2048 25 each.
-static bool few_tokens(const LinearArgs &a) {
-    return a.tokens <= QSDP_LINEAR_EXACT_TOKENS ||
-           (a.tokens <= 64 && whole_steps(a) && a.rows * a.cols >= int64_t{1} << 26);
-}
+// Few tokens go to the streaming kernel: 32 over 28672 x 8192 49 us against the tiles' 84, over 8192 x 4096
+// 15 to 16 against 24, over 4096 x 4096 14 against 18 (but 8 bits over 20000 x 1600 24 against 18).  With 33
+// to 64 the tiles are ahead (16384 x 8192 52 us against 70, 8 bits over 28672 x 8192 102 against 129; 4 bits 89
+// against 78).
+static bool few_tokens(const LinearArgs &a) { return a.tokens <= QSDP_LINEAR_EXACT_TOKENS; }
 
 template <int GT, int BITS>
 static void launch_rows_groups(const LinearArgs &a, hipStream_t s) {
-    if (whole_steps(a))
+    // whether every step of a row has one bucket
+    if (a.cols % kRowsChunk == 0 && a.bucket % kRowsChunk == 0)
         launch_rows_tiles<GT, BITS, 1>(a, s);
     else
         launch_rows_tiles<GT, BITS, 4>(a, s);

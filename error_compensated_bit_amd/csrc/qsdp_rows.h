@@ -14,7 +14,7 @@
 // them x, which goes through LDS too; groups share the columns of the same rows among them and
 // add up in LDS at the end.
 //
-// Measured (a copy moves 4.8 TB/s): 32 tokens over 28672 x 8192, 4 bits, 50 us for 134 MB (2.7 TB/s);
+// Measured (a copy moves 4.8 TB/s): 32 tokens over 28672 x 8192, 4 bits, 48 to 52 us for 134 MB (2.7 TB/s);
 // 5 over 50257 x 1600, 8 bits, buckets of 1024, 25 to 28 us for 82 MB; one over 6400 x 1600, 4 bits, 6.7
 // us, of which a launch is 4.  Without its products the first takes 40, the second 26: what the loop
 // reads, 128 bytes of eight rows at a time, comes at 3.3 to 4 TB/s (alone, in a probe, 5).
@@ -155,7 +155,7 @@ __global__ __launch_bounds__(64 * WAVES * SPLIT) void k_qsdp_rows(LinearArgs a) 
     const int begin = group * each, end = min(begin + each, steps);
 
     // Rows by their offsets from the wave's first (behind the last row: the last one again, not
-    // written), buckets by their numbers from that row's first.  Every offset fits 32 bits: 64 rows
+    // written), buckets by their numbers from that row's first.  Every offset fits 32 bits: 32 rows
     // of less than 2^24 codes, and buckets of at least 32.
     const int64_t first_row = uniform(min(row0, a.rows - 1));
     const uint32_t row_parts = (uint32_t)(a.cols >> 5), bucket_parts = (uint32_t)a.bucket >> 5;

@@ -139,6 +139,23 @@ def test_large_matrices(rows, cols, bits, bucket, dtype):
         assert torch.equal(run("linear", padded(x), weights, rows, cols, bucket, bits), want), tokens
 
 
+# each number of the matrix's rows that a workgroup of the streaming kernel takes, with one bucket of a row's
+# 128 columns and with several; rows that end inside a workgroup's
+@pytest.mark.parametrize("rows,cols", [(4095, 640), (4097, 384), (8193, 384), (9000, 1120), (20001, 256), (32771, 128),
+                                       (32800, 1440)])
+@pytest.mark.parametrize("bits,bucket", [(4, 128), (4, 96), (8, 256), (8, 1024)])
+@pytest.mark.parametrize("dtype", [BF16, F16])
+def test_few_tokens_times_many_rows(rows, cols, bits, bucket, dtype):
+    for tokens in (1, 16, 17, 32):
+        g = gen("few", rows, cols, bits, bucket, tokens)
+        weights = coded(rows, cols, bucket, bits, g)
+        x = torch.randn(tokens, cols, generator=g).to(dtype)
+        want, tol = expect("linear", x.to(DEV), weights, rows, cols, bucket, bits)
+        got = run("linear", padded(x), dev(weights), rows, cols, bucket, bits)
+        off = (got.double() - want).abs() / tol
+        assert torch.all(off <= 1.0), (tokens, float(off.max()))
+
+
 @pytest.mark.parametrize("tokens", [5, 40, 130])
 @pytest.mark.parametrize("bits", [4, 8])
 def test_gradient_is_the_products_differences(tokens, bits):
