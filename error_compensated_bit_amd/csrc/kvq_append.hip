@@ -165,6 +165,11 @@ extern "C" onebit_status_t kvq_append(const void *q, const void *k, const void *
     if (q_heads > 0 && (!aligned16(q) || !aligned16(q_out) || q_token_stride % unit || q_head_stride % unit ||
                         out_token_stride % unit || out_head_stride % unit))
         return ONEBIT_ERR_ALIGN;
+    // rows of the result that would overlap
+    const int dim = cache->head_dim;
+    if (q_heads > 0 && ((tokens > 1 && out_token_stride > -dim && out_token_stride < dim) ||
+                        (q_heads > 1 && out_head_stride > -dim && out_head_stride < dim)))
+        return ONEBIT_ERR_INVALID;
     a.src[0] = q;
     a.src[1] = k;
     a.src[2] = v;

@@ -53,8 +53,8 @@ __device__ __forceinline__ Bucket bucket_of(int64_t p, uint32_t bucket_parts) {
 }
 
 // fl32(fl32(hi - lo) / (2^BITS - 1)): the product with the rounded reciprocal, corrected once by its
-// exact remainder, is the correctly rounded quotient (Markstein); infinities and NaN stay
-// what they are not finite for.
+// exact remainder, is the correctly rounded quotient (Markstein).  A range that is not finite
+// gives NaN.
 template <int BITS>
 __device__ __forceinline__ float bucket_delta(float lo, float hi) {
     constexpr float kLevels = (float)((1 << BITS) - 1), kInv = 1.0f / kLevels;

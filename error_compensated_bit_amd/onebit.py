@@ -517,7 +517,7 @@ def _linear(name, x, y, rows, cols, codes, bucket_min, bucket_max, bucket, bits,
 
 
 def qsdp_linear_workspace_bytes(tokens, rows, cols) -> int:
-    """Bytes for the current device, for qsdp_linear and qsdp_linear_grad; 0 for sizes that they refuse."""
+    """Bytes for qsdp_linear or qsdp_linear_grad; 0 for sizes that they refuse."""
     return int(load().qsdp_linear_workspace_bytes(int(tokens), int(rows), int(cols)))
 
 

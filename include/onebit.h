@@ -438,7 +438,7 @@ typedef struct {
  * elements, 16-byte aligned base, stride a multiple of 8 (ONEBIT_ERR_ALIGN otherwise), at
  * least the row's length and below 2^23; what lies between two rows is never used.  out, dx: the
  * same type, any stride of at least the row's length and below 2^32; what lies between two
- * rows stays as it was.  (A single row's stride is not looked at.)  0 <= tokens < 2^24; no tokens:
+ * rows stays as it was.  Results must not overlap anything that the call reads, nor the workspace.  (A single row's stride is not looked at.)  0 <= tokens < 2^24; no tokens:
  * the call does nothing.
  * Sums are binary32.  Roundings before them: none in qsdp_linear with up to
  * QSDP_LINEAR_EXACT_TOKENS tokens, where codes and minima enter apart; else of the weights
@@ -448,7 +448,8 @@ typedef struct {
  * A value of x or dy that is not finite leaves nothing finite in its own row of the result and
  * makes no difference to the others; a bucket whose minimum or maximum is not finite leaves
  * nothing finite in the results that use its weights, and makes no difference to the others.
- * (Sums of |x| over a row times 2^9 of its largest delta are to stay below 2^127.)
+ * (The sum of |x| over a row, times 2^9 and times the largest delta or |minimum|, where these are above 1,
+ * is to stay below 2^127.)
  * workspace: qsdp_linear_workspace_bytes bytes (for either call), 16-byte aligned; what it
  * holds before a call does not matter.  Calls that may overlap in time need one each, and
  * so do two captured graphs that may be replayed at the same time.  (0 is returned for
@@ -527,7 +528,8 @@ onebit_status_t kvq_quantize(const void *k, const void *v, onebit_dtype_t dtype,
  * cache as it is; its token's queries are rotated all the same.
  * No slot may occur twice in a call.  Tokens, k, v, slots: as in kvq_quantize, and q and
  * q_out addressed as k is, of the same type.  q_out may be q itself (same strides) and must not
- * overlap q otherwise.  q_heads from 0 (q and q_out are not used) to 32767; rot_dim a
+ * overlap q otherwise, nor anything else that the call reads or writes; nor may its rows overlap each other
+ * (ONEBIT_ERR_INVALID where the stride of several tokens or heads is within head_dim of 0).  q_heads from 0 (q and q_out are not used) to 32767; rot_dim a
  * multiple of 16 from 16 to head_dim; max_position >= 1 and max_position * rot_dim < 2^47;
  * rotary 16-byte aligned. */
 onebit_status_t kvq_append(const void *q, const void *k, const void *v, onebit_dtype_t dtype, int64_t tokens,

@@ -42,6 +42,13 @@ def test_refusals(kw, status):
     assert append(**kw) == status
 
 
+@pytest.mark.parametrize("stride", [0, 64, 120, -120])
+def test_rows_of_the_result_that_overlap_are_refused(stride):
+    assert append(ot=stride) == INV
+    assert append(oh=stride) == INV
+    assert append(tokens=1, oh=stride) == INV
+
+
 def test_null_cache_is_refused():
     assert ob.load().kvq_append(A, A, A, 1, 3, 4, 512, 128, 256, 128, 256, 128, A, A, 100, 128, 0, A, None, A, 512, 128,
                                 None) == INV
