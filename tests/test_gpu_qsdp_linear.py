@@ -412,3 +412,15 @@ def test_bindings_refusals():
                       (ob.OnebitError, dict(x=x[:1].expand(3, cols)))]:
         with pytest.raises(error):
             call(**kw)
+
+
+@pytest.mark.parametrize("tokens,rows,cols", [(1, 20011, 96), (17, 9434, 64), (70, 12001, 320), (500, 50257, 160)])
+@pytest.mark.parametrize("bits,bucket", [(4, 1024), (8, 96)])
+@pytest.mark.parametrize("dtype", [BF16, F16])
+def test_gradient_over_many_rows(tokens, rows, cols, bits, bucket, dtype):
+    """Few tiles, whose depth many workgroups share."""
+    g = gen("deep", tokens, rows, cols, bits)
+    weights = dev(coded(rows, cols, bucket, bits, g))
+    x = torch.randn(tokens, rows, generator=g).to(dtype)
+    want, tol = expect("grad", x.to(DEV), weights, rows, cols, bucket, bits)
+    assert torch.all((run("grad", padded(x), weights, rows, cols, bucket, bits).double() - want).abs() <= tol)
