@@ -233,6 +233,8 @@ __global__ __launch_bounds__(64 * WAVES * SPLIT) void k_qsdp_rows(LinearArgs a) 
                 const uint4 &v = w[slot + (kSteps == 2 ? k : 0)][t][kSteps == 2 ? 0 : k];
                 s_w[128 * t + 64 * k + (lane ^ (lane >> 3))] = (u32x4_v){v.x, v.y, v.z, v.w};
             }
+        // (what other lanes wrote is read: nothing else tells the compiler of the order)
+        __builtin_amdgcn_wave_barrier();
 #pragma unroll
         for (int t = 0; t < NT; ++t)
 #pragma unroll
