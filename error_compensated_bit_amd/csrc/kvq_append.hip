@@ -88,6 +88,8 @@ __global__ __launch_bounds__(kAppendBlock) void k_kvq_append(KvqAppendArgs a) {
             }
         }
     }
+    // (q_out may be q: rows are read by all of their lanes before one writes)
+    __builtin_amdgcn_wave_barrier();
     const bool ok = live && slot >= 0 && slot < a.c.n_slots;
     const int64_t at_page = ok ? slot >> a.c.shift : 0;
     const int32_t in_page = ok ? (int32_t)(slot & (a.c.page - 1)) : 0;

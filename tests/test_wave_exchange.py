@@ -46,6 +46,21 @@ def test_codes_turned_through_lds():
     assert seen == 2
 
 
+def test_queries_turned_in_place():
+    """All of a row is read before any of it is written."""
+    seen = 0
+    for name, listing in kernels("k_kvq_append"):
+        if "ILi1ELi128ELi8E" not in name:
+            continue
+        stores = [i for i, op in enumerate(listing) if op.startswith("global_store")]
+        loads = [i for i, op in enumerate(listing) if op.startswith("global_load")]
+        fences = [i for i, op in enumerate(listing) if op == "; wave barrier"]
+        assert stores and loads and max(loads) < min(stores), name
+        assert any(max(loads) < i < min(stores) for i in fences), name
+        seen += 1
+    assert seen == 1
+
+
 def test_the_check_itself():
     assert unfenced(["ds_write_b128", "ds_read_b128", "ds_read_b128"]) == 2
     assert unfenced(["ds_write_b128", "; wave barrier", "ds_read_b128", "s_barrier", "ds_read_b32"]) == 0
