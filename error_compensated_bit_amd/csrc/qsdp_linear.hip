@@ -39,7 +39,7 @@ static void launch_rows_tiles(const LinearArgs &a, hipStream_t s) {
 // 15 to 16 against 24, over 4096 x 4096 14 against 18 (but 8 bits over 20000 x 1600 24 against 18).  With 33
 // to 64 the tiles are ahead (16384 x 8192 52 us against 70, 8 bits over 28672 x 8192 102 against 129; 4 bits 89
 // against 78).
-static bool few_tokens(const LinearArgs &a) { return a.tokens <= QSDP_LINEAR_EXACT_TOKENS; }
+static bool few_tokens(int64_t tokens) { return tokens <= QSDP_LINEAR_EXACT_TOKENS; }
 
 template <int GT, int BITS>
 static void launch_rows_groups(const LinearArgs &a, hipStream_t s) {
@@ -117,7 +117,7 @@ static void launch_tile(const TileArgs &a, hipStream_t s) {
 
 template <int GT, int BITS, bool GRAD>
 static void launch(const LinearArgs &l, hipStream_t s) {
-    if (!GRAD && few_tokens(l)) return launch_rows_groups<GT, BITS>(l, s);
+    if (!GRAD && few_tokens(l.tokens)) return launch_rows_groups<GT, BITS>(l, s);
     TileArgs a{};
     a.l = l;
     a.depth = GRAD ? l.rows : l.cols;
@@ -145,10 +145,14 @@ static void dispatch(onebit_dtype_t dtype, int bits, const LinearArgs &a, hipStr
 
 constexpr int64_t kLinearMost = 1 << 24;  // tokens, rows and columns are below
 
+// Bytes that a call with a result of `width` columns uses at most; no fewer with more tokens.
+static size_t linear_need(bool grad, int64_t tokens, int64_t width) {
+    return !grad && few_tokens(tokens) ? 16 : (size_t)std::max(partial_room(tokens, width), int64_t{16});
+}
 static size_t linear_workspace(int64_t tokens, int64_t rows, int64_t cols) {
     if (tokens < 0 || tokens >= kLinearMost || rows < 1 || rows >= kLinearMost || cols < 32 || cols >= kLinearMost || cols % 32)
         return 0;
-    return (size_t)std::max(partial_room(tokens, std::max(rows, cols)), int64_t{16});
+    return std::max(linear_need(false, tokens, rows), linear_need(true, tokens, cols));
 }
 
 template <bool GRAD>
@@ -166,7 +170,7 @@ static onebit_status_t linear(const void *x, onebit_dtype_t dtype, int64_t token
     if (!x || !out || !workspace || !w->codes || !w->bucket_min || !w->bucket_max) return ONEBIT_ERR_INVALID;
     if (tokens > 1 && (x_stride < depth || out_stride < width || x_stride >= int64_t{1} << 23 || out_stride >= int64_t{1} << 32))
         return ONEBIT_ERR_INVALID;
-    if (workspace_bytes < linear_workspace(tokens, w->rows, w->cols)) return ONEBIT_ERR_INVALID;
+    if (workspace_bytes < linear_need(GRAD, tokens, width)) return ONEBIT_ERR_INVALID;
     if (!aligned16(x) || (tokens > 1 && x_stride % 8) || !aligned_to(out, 2) || !aligned16(workspace) || !aligned16(w->codes) ||
         !aligned_to(w->bucket_min, 4) || !aligned_to(w->bucket_max, 4))
         return ONEBIT_ERR_ALIGN;

@@ -517,7 +517,9 @@ def _linear(name, x, y, rows, cols, codes, bucket_min, bucket_max, bucket, bits,
 
 
 def qsdp_linear_workspace_bytes(tokens, rows, cols) -> int:
-    """Bytes for qsdp_linear or qsdp_linear_grad; 0 for sizes that they refuse."""
+    """Bytes for qsdp_linear or qsdp_linear_grad, also with fewer tokens; 0 for sizes that they refuse.  The
+    first alone takes 16 bytes with up to QSDP_LINEAR_EXACT_TOKENS tokens and those of cols = 32 with
+    more, the second alone those of rows = 1."""
     return int(load().qsdp_linear_workspace_bytes(int(tokens), int(rows), int(cols)))
 
 

@@ -450,8 +450,11 @@ typedef struct {
  * nothing finite in the results that use its weights, and makes no difference to the others.
  * (The sum of |x| over a row, times 2^9 and times the largest delta or |minimum|, where these are above 1,
  * is to stay below 2^127.)
- * workspace: qsdp_linear_workspace_bytes bytes (for either call), 16-byte aligned; what it
- * holds before a call does not matter.  Calls that may overlap in time need one each, and
+ * workspace: 16-byte aligned; what it holds before a call does not matter.
+ * qsdp_linear_workspace_bytes bytes are enough for either call, also with fewer tokens.  One
+ * call alone takes less: qsdp_linear 16 bytes with up to QSDP_LINEAR_EXACT_TOKENS tokens and
+ * qsdp_linear_workspace_bytes(tokens, rows, 32) with more, qsdp_linear_grad
+ * qsdp_linear_workspace_bytes(tokens, 1, cols).  Calls that may overlap in time need one each, and
  * so do two captured graphs that may be replayed at the same time.  (0 is returned for
  * sizes that the calls refuse.)  The calls are not among the classes of the launch timing above. */
 #define QSDP_LINEAR_EXACT_TOKENS 32
