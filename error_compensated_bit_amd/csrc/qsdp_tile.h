@@ -20,10 +20,9 @@
 #pragma once
 
 #include "qsdp_linear.h"
+#include "qsdp_plan.h"
 
 namespace onebit {
-
-constexpr int kTileDepth = 64;
 
 // TM x TN results of a workgroup, WM x WN of a wave; GROUPS of waves share the depth, each with
 // buffers of its own; AHEAD steps of a group are on their way from memory.
