@@ -30,6 +30,29 @@ def tile_weights(codes, lo, hi, rows, cols, bucket, bits, dtype):
     return w.float().to(dtype).double().view(rows, cols)
 
 
+def tile_product(op, x, w):
+    """(result in fp64, elementwise tolerance) of x [tokens, depth] with tile_weights' w [rows, cols].
+
+    The tolerance counts the result's own rounding (half a step, of the smallest normal number at least) and
+    the sums in fp32.  Let P be the largest magnitude of a sum over the first 64 k products, for any k, and
+    L the largest sum of 64 products' magnitudes.  What is added up is always a stretch of whole blocks and
+    part of another, so every partial sum is within 2 P + L, and a rounding to fp32 within 2^-24 of
+    that.  depth + 64 of them (one for each product, the joins of groups and shares), taken as
+    independent: eight times the root of their number.  (Products of values of 11 bits are exact.)"""
+    if op == "linear":
+        w = w.t().contiguous()
+    dtype, x, depth = x.dtype, x.double(), x.shape[1]
+    y = torch.zeros(x.shape[0], w.shape[1], dtype=torch.float64, device=x.device)
+    most, block = torch.zeros_like(y), torch.zeros_like(y)
+    for d in range(0, depth, 64):
+        a, b = x[:, d:d + 64].contiguous(), w[d:d + 64]
+        y = torch.addmm(y, a, b)
+        most = torch.maximum(most, y.abs())
+        block = torch.maximum(block, a.abs() @ b.abs())
+    tol = ref.HALF_STEP[dtype] * y.abs().clamp_min(torch.finfo(dtype).tiny)
+    return y, tol + 8.0 * (depth + 64) ** 0.5 * 2.0 ** -24 * (2.0 * most + block)
+
+
 def coded_weights(rows, cols, bucket, bits, g, whole=False):
     """Codes, minima and maxima as the products' tests draw them.  whole: small whole weights, at most 155 in
     magnitude and exact in 8 bits of mantissa."""

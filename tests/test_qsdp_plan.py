@@ -1,5 +1,5 @@
 """How the tiled products with coded weights are cut up (host code of the library's header, compiled
-and run here)."""
+and run here), and what the GPU tests' tolerance can see."""
 import ctypes as C
 import math
 import os
@@ -8,7 +8,9 @@ import shutil
 import subprocess
 
 import pytest
+import torch
 
+import qsdp_linear_ref as ref
 import qsdp_tile_ref as tiles
 from error_compensated_bit_amd import onebit as ob
 
@@ -75,3 +77,35 @@ def test_the_gpu_tests_sizes_reach_every_tile():
     have = {(op, shape, splits > 1) for op, _, _, _, shape, splits in tiles.PLANNED}
     # (the largest tile alone, forward, is what the tests of many tokens take)
     assert have >= {(op, s, shared) for op in ("linear", "grad") for s in range(4) for shared in (False, True)} - {("linear", 0, False)}
+
+
+@pytest.mark.parametrize("op,tokens,rows,cols", [("grad", 40, 50257, 32), ("grad", 1, 20011, 96), ("linear", 70, 40, 12000),
+                                                 ("grad", 130, 8192, 64)])
+@pytest.mark.parametrize("bits,bucket", [(4, 1024), (8, 96)])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+def test_the_tolerance_sees_a_step_left_out(op, tokens, rows, cols, bits, bucket, dtype):
+    """One step of 64 missing from the sum: most results are off by more than the tolerance."""
+    g = torch.Generator().manual_seed(rows + bits)
+    w = tiles.tile_weights(*tiles.coded_weights(rows, cols, bucket, bits, g), rows, cols, bucket, bits, dtype)
+    depth = cols if op == "linear" else rows
+    x = torch.randn(tokens, depth, generator=g).to(dtype)
+    y, tol = tiles.tile_product(op, x, w)
+    at = depth // 128 * 64
+    short = x.clone()
+    short[:, at:at + DEPTH] = 0
+    off = (tiles.tile_product(op, short, w)[0] - y).abs() / tol
+    assert (off > 1.0).double().mean() > 0.5
+    # and the product's own rounding stays inside
+    assert torch.all((y.to(dtype).double() - y).abs() <= tol)
+
+
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+def test_rounded_weights_are_within_half_a_step(bits, dtype):
+    g = torch.Generator().manual_seed(bits)
+    coded = tiles.coded_weights(70, 96, 64, bits, g)
+    w, _ = ref.weights(*coded, 70, 96, 64, bits)
+    r = tiles.tile_weights(*coded, 70, 96, 64, bits, dtype)
+    half = ref.HALF_STEP[dtype]
+    # (rounded to fp32 first: half a step of that more; fp16 below 2^-14 is held to 2^-25)
+    assert torch.all((r - w).abs() <= (half + 2.0 ** -24) * w.abs() + (2.0 ** -25 if dtype == torch.float16 else 0.0))
