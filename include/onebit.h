@@ -440,11 +440,16 @@ typedef struct {
  * same type, any stride of at least the row's length and below 2^32; what lies between two
  * rows stays as it was.  Results must not overlap anything that the call reads, nor the workspace.  (A single row's stride is not looked at.)  0 <= tokens < 2^24; no tokens:
  * the call does nothing.
- * Sums are binary32.  Roundings before them: none in qsdp_linear with up to
- * QSDP_LINEAR_EXACT_TOKENS tokens, where codes and minima enter apart; else of the weights
- * to the type of x or dy, nearest even (for fp16, weights above 65504 become infinite).  A bucket
- * has 2^bits weights, so equal codes' errors are equal: a result is off by half a step of the
- * type times sum |x w| at most, and by less only as far as the signs of x differ.
+ * Sums are binary32, and a result is rounded once to its type.  Roundings before the sums:
+ *  - qsdp_linear with up to QSDP_LINEAR_EXACT_TOKENS tokens: codes and minima enter apart, exact but for
+ *    fl32(min_b - 16 delta_b) (4 bits) or fl32(min_b + 128 delta_b) (8 bits, fp16), which stands in
+ *    for the minimum.  (Who needs this for more tokens calls with so many at a time.)
+ *  - else each weight, formed by one fused operation (fl32(min_b + code * delta_b), where
+ *    qsdp_dequantize rounds the product too), is rounded to the type of x or dy, nearest even.  A bucket
+ *    has 2^bits weights, so equal codes' errors are equal: these add half a step of the type times
+ *    sum |x w| to a result's error at most, and less only as far as the signs of x differ.  In fp16
+ *    a weight below 2^-14 is off by 2^-25 at most, and one of 65520 or more becomes infinite, which leaves
+ *    nothing finite in the results that use it.
  * A value of x or dy that is not finite leaves nothing finite in its own row of the result and
  * makes no difference to the others; a bucket whose minimum or maximum is not finite leaves
  * nothing finite in the results that use its weights, and makes no difference to the others.
