@@ -416,6 +416,9 @@ onebit_status_t qsdp_mean_abs_error(const uint16_t *x_bf16, const double *ysum, 
  *   w_{o,i} = min_b + code * delta_b,  b = (o * cols + i) / bucket,
  * with delta_b as above; buckets may run across rows.
  *   codes, bucket_min, bucket_max: as qsdp_quantize wrote them for n values.
+ *   Shards that were quantized by themselves and gathered one behind another are such a vector
+ *   only if every shard but the last is a whole number of buckets long: a shard's first bucket
+ *   begins where the shard does.  (Nothing in the arrays tells; other shards are a matrix each.)
  *   cols and bucket are multiples of 32 (ONEBIT_ERR_UNSUPPORTED otherwise), bucket <= 65536;
  *   rows >= 1, cols >= 32, both below 2^24.  codes 16-byte aligned.
  * The struct is a host struct, read during the call. */
