@@ -11,7 +11,8 @@
 // bytes, are read once for them.
 //
 // Measured: 16384 tokens of 32 + 2 x 8 heads of 128, bf16, 4 bits, 83 to 90 us for 362 MB (4.0 to 4.4 TB/s;
-// a copy moves 4.8); 5003 of 16 + 2 x 16 heads of 64, fp16, 8 bits, 13.6 us; 64 tokens 5.3 us.
+// a copy moves 4.8), fp32 164 us for 698 MB; 5003 of 16 + 2 x 16 heads of 64, fp16, 8 bits, 13.6 us; 64 tokens 5.3
+// us (fp32 4.8, in a graph).
 #include "kvq_rows.h"
 
 namespace onebit {
@@ -134,6 +135,8 @@ struct AppendLaunch {
     hipStream_t s;
     template <int GT, int D, int BITS>
     void run() const {
+        // at least 8 tokens of fewer than 2^26: at most 2^31 threads along x; at most 3 * 32767 heads, four
+        // each: at most 24576 workgroups along y
         constexpr int64_t each = kAppendBlock / (D / 8);
         const int heads = a.q_heads + 2 * a.c.heads;
         const dim3 grid((unsigned)((a.tokens + each - 1) / each), (heads + kAppendHeads - 1) / kAppendHeads);

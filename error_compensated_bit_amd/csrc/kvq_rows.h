@@ -113,8 +113,8 @@ inline void kvq_dispatch(onebit_dtype_t dtype, int dim, int bits, F f) {
         kvq_dispatch_dim<kGradF16>(dim, bits, f);
 }
 
-// Checks shared by the calls over rows.  The grid has ceil(tokens / rows) x 2 heads workgroups
-// of at least 32 rows: fewer than 2^32 threads along x, at most 65535 workgroups along y.
+// Checks shared by the calls over rows.  They bound the grids: kvq_quantize and kvq_dequantize have
+// ceil(tokens / rows) x 2 heads workgroups of at least 32 rows, kvq_append is bounded at its own launch.
 inline onebit_status_t kvq_check_rows(const kvq_cache_t *cache, onebit_dtype_t dtype, int64_t tokens, KvqCache *out) {
     if (dtype != ONEBIT_F32 && dtype != ONEBIT_BF16 && dtype != ONEBIT_F16) return ONEBIT_ERR_INVALID;
     if (tokens < 0 || tokens >= (1 << 26)) return ONEBIT_ERR_INVALID;

@@ -35,12 +35,17 @@ constexpr PlannedShape kPlannedShapes[4] = {
     {256, 256, 1, {2.4f, 2.4f}}, {128, 128, 2, {1.55f, 1.9f}}, {64, 128, 2, {1.25f, 1.4f}}, {64, 64, 4, {1.6f, 1.8f}}};
 
 // The cheapest by this estimate (us): a workgroup is alone on its compute unit, so there are as many rounds of
-// workgroups as 256 go into them, of so many steps each.  What a step takes was measured with 4-bit
-// codes, linear / gradient: first shape 2.4 (2048 x 16384 x 4096: 300 us in 2 x 64 steps) / 2.4 (500 x
-// 1600 x 50257, 16 workgroups a tile: 144 in 50), second 1.55 (1000 x 4096 x 4096: 53 in 32) / 1.9 (4096
-// x 1600 x 6400: 193 in 2 x 50), third 1.25 (333 x 4800 x 1600: 19 in 13) / 1.4 (512 x 4096 x 4096: 48
-// in 32), fourth 1.6 / 1.8 (the same: 63 in 2 x 16).  Sharing a tile's depth costs a second launch and
-// the partial results' way to memory and back: 2.5 us and 3 us for every 8 MB.
+// workgroups as 256 (the whole GPU's units) go into them, of so many steps each.  The steps' times above are
+// those of an earlier state of the kernels; what a step takes now, of whole calls in bf16 with 4 / 8 bits:
+//   first shape   linear 2.2 / 2.1 (2048 x 16384 x 4096: 277 / 266 us in 2 x 64 steps), gradient 2.2 / 2.1 (4096 x
+//                 1600 x 6400, 2 workgroups a tile: 121 / 118 in 50 and a join of 13) and 2.4 / 2.3 (500 x 1600
+//                 x 50257, 16 of them: 134 / 124 in 50 and a join of 12)
+//   second shape  linear 1.7 (1000 x 4096 x 4096: 56 in 32), gradient 1.7 / 1.6 (4096 x 1600 x 6400: 166 / 157 in 2 x 50)
+//   third shape   linear 1.3 (512 x 4096 x 4096: 41 in 32; 333 x 4800 x 1600: 17 in 13), gradient 1.5 / 1.4 (512 x
+//                 4096 x 4096: 46 / 44 in 32)
+//   fourth shape  linear 1.6 (512 x 4096 x 4096: 50 in 2 x 16), gradient 1.9 (the same: 62 / 60)
+// Choices up to 14% from the best one are known (787 x 7392 x 4551: 116 against 101.5 us).  Sharing a tile's depth
+// costs a second launch and the partial results' way to memory and back: 2.5 us and 3 us for every 8 MB.
 inline TilePlan tile_plan(int64_t tokens, int64_t width, int64_t depth, bool grad) {
     const int64_t steps = (depth + kTileDepth - 1) / kTileDepth;
     const int64_t room = partial_room(tokens, width);

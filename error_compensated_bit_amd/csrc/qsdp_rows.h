@@ -1,10 +1,10 @@
 // qsdp_rows.h -- few rows times a coded matrix: bound by reading the codes, once.
 //   out_{t,o} = sum_b [ delta_b sum_{i in b} x_{t,i} c_i + min_b sum_{i in b} x_{t,i} ]
 // with the sums over a bucket's part of row o.  Codes enter the matrix cores as whole
-// numbers (4 bits: 16 + c, by a shift and a mask for two; 8 bits: c, or c - 128 in fp16), so
-// nothing but the fp32 sums and the result is rounded, and what the offset adds is taken
-// back through the bucket's minimum: min' = min - offset * delta.  The sums of x alone come
-// from one more product, with ones.
+// numbers (4 bits: 16 + c, by a shift and a mask for two; 8 bits: c, or c - 128 in fp16), and
+// what the offset adds is taken back through the bucket's minimum: min' = fl32(min - offset *
+// delta).  Beside that nothing but the fp32 sums and the result is rounded.  The sums of x
+// alone come from one more product, with ones.
 //
 // v_mfma_f32_16x16x32 with x's rows along the first side and rows of the matrix along the
 // second: a lane holds one matrix row's results, so it needs the deltas of that row only.
@@ -14,10 +14,12 @@
 // them x, which goes through LDS too; groups share the columns of the same rows among them and
 // add up in LDS at the end.
 //
-// Measured (a copy moves 4.8 TB/s): 32 tokens over 28672 x 8192, 4 bits, 48 to 52 us for 134 MB (2.7 TB/s);
-// 5 over 50257 x 1600, 8 bits, buckets of 1024, 25 to 28 us for 82 MB; one over 6400 x 1600, 4 bits, 6.7
-// us, of which a launch is 4.  Without its products the first takes 40, the second 26: what the loop
-// reads, 128 bytes of eight rows at a time, comes at 3.3 to 4 TB/s (alone, in a probe, 5).
+// Measured (a copy moves 4.8 to 4.95 TB/s): 32 tokens over 28672 x 8192, 4 bits, 48 to 52 us for 134 MB (2.7
+// TB/s), 54 with codes that no cache holds; 5 over 50257 x 1600, 8 bits, buckets of 1024, 25 to 28 us for 82 MB
+// (cold 28); one over 8192 x 8192, 4 bits, 15 us for 38 MB (cold 17), over 6400 x 1600 6.0 to 6.7 us, of which a
+// launch is 4.  Without its products the first takes 40, the second 26: what the loop reads, 128 bytes of eight
+// rows at a time, comes at 3.1 to 3.3 TB/s (alone, in a probe, 5).  The matrix cores are busy in 23% and 11% of the
+// compute units' time, LDS in 31% and 33%.
 #pragma once
 
 #include "qsdp_linear.h"

@@ -4,6 +4,11 @@
 // A workgroup has TM x TN results and goes through the depth in steps of 64.  A step's x
 // and its weights, expanded once for all TM rows and rounded to x's type, lie in LDS twice over:
 // while one is multiplied the next is written and the one after that is on its way from memory.
+// The matrix cores take both operands in one type, so a weight is rounded to 8 or 11 bits: a second
+// product with what the rounding leaves would double the products (floor of 2048 x 16384 x 4096: 200 us,
+// then 400) and the weights' half of LDS, which the first shape does not have.  What that costs, against
+// 64 bits in root mean square: 0.0023 instead of the result's own 0.0017 in bf16, 0.00029 instead of
+// 0.00021 in fp16.
 // Each wave writes first and multiplies then: of two waves on a SIMD one comes to its products
 // while the other still expands (half of them the other way round: twice the code, and no faster).
 //
@@ -13,10 +18,12 @@
 // addresses differ by a constant.  An operand of v_mfma_f32_16x16x32 is one piece of 16 rows.  Weights are the first
 // operand, so that a lane holds four neighbouring results of one row of x.
 //
-// Measured: 2048 x 16384 x 4096, 4 bits, bf16, 278 to 290 us (0.95 to 0.99 PFLOP/s; the library's product
-// with decoded weights, 200); gradient of 4096 x 1600 x 6400 129 us (97), of 500 x 1600 x 50257, fp16,
-// 8 bits, 130 us (269).  Small products are bound by a step's chain of waits, 1.2 us: 333 x 4800 x
-// 1600 17 us, 77 x 4096 x 4096 19.
+// Measured: 2048 x 16384 x 4096, 4 bits, bf16, 260 to 290 us (0.95 to 1.06 PFLOP/s; the library's product
+// with decoded weights, 179 to 200); gradient of 4096 x 1600 x 6400 120 to 126 us (87 to 97), of 500 x 1600 x
+// 50257, fp16, 8 bits, 120 to 132 us (270).  In the first the matrix cores are busy in 44% of the compute
+// units' time, LDS in 44% and in 17% for bank conflicts; in the gradients 42%, 48% and 16%.
+// Small products are bound by a step's chain of waits, 1.2 us: 333 x 4800 x 1600 17 us, 77 x 4096 x 4096
+// 18 to 20 (matrix cores 15%).
 #pragma once
 
 #include "qsdp_linear.h"
