@@ -441,8 +441,9 @@ typedef struct {
  * elements, 16-byte aligned base, stride a multiple of 8 (ONEBIT_ERR_ALIGN otherwise), at
  * least the row's length and below 2^23; what lies between two rows is never used.  out, dx: the
  * same type, any stride of at least the row's length and below 2^32; what lies between two
- * rows stays as it was.  Results must not overlap anything that the call reads, nor the workspace.  (A single row's stride is not looked at.)  0 <= tokens < 2^24; no tokens:
- * the call does nothing.
+ * rows stays as it was.  Results must not overlap anything that the call reads, nor the
+ * workspace.  (A single row's stride is not looked at.)  0 <= tokens < 2^24; no tokens: the call
+ * does nothing.
  * Sums are binary32, and a result is rounded once to its type.  Roundings before the sums:
  *  - qsdp_linear with up to QSDP_LINEAR_EXACT_TOKENS tokens: codes and minima enter apart, exact but for
  *    fl32(min_b - 16 delta_b) (4 bits) or fl32(min_b + 128 delta_b) (8 bits, fp16), which stands in
@@ -539,10 +540,10 @@ onebit_status_t kvq_quantize(const void *k, const void *v, onebit_dtype_t dtype,
  * cache as it is; its token's queries are rotated all the same.
  * No slot may occur twice in a call.  Tokens, k, v, slots: as in kvq_quantize, and q and
  * q_out addressed as k is, of the same type.  q_out may be q itself (same strides) and must not
- * overlap q otherwise, nor anything else that the call reads or writes; nor may its rows overlap each other
- * (ONEBIT_ERR_INVALID where the stride of several tokens or heads is within head_dim of 0).  q_heads from 0 (q and q_out are not used) to 32767; rot_dim a
- * multiple of 16 from 16 to head_dim; max_position >= 1 and max_position * rot_dim < 2^47;
- * rotary 16-byte aligned. */
+ * overlap q otherwise, nor anything else that the call reads or writes; nor may its rows overlap
+ * each other (ONEBIT_ERR_INVALID where the stride of several tokens or heads is within head_dim
+ * of 0).  q_heads from 0 (q and q_out are not used) to 32767; rot_dim a multiple of 16 from 16 to
+ * head_dim; max_position >= 1 and max_position * rot_dim < 2^47; rotary 16-byte aligned. */
 onebit_status_t kvq_append(const void *q, const void *k, const void *v, onebit_dtype_t dtype, int64_t tokens,
                            int q_heads, int64_t q_token_stride, int64_t q_head_stride, int64_t k_token_stride,
                            int64_t k_head_stride, int64_t v_token_stride, int64_t v_head_stride,
