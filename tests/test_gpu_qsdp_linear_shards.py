@@ -21,7 +21,7 @@ def quantized(x, bucket, bits, seed):
 @pytest.mark.parametrize("rows,cols,cuts,bucket", [
     (96, 160, (5120, 10240), 1024),            # shards that end inside rows
     (96, 160, (4800, 9600), 32),               # whole rows, the finest buckets
-    (50, 96, (1536, 3072), 96),                # a short last shard
+    (50, 96, (1536, 2880), 96),                # a short last shard
 ])
 def test_gathered_shards(bits, rows, cols, cuts, bucket):
     g = gen("shards", rows, bits)
